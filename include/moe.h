@@ -476,4 +476,7 @@ int moe_combine(const uint16_t *y, int M, int N, int top_k, uint16_t *out,
 #ifdef __cplusplus
 }
 #endif
+
+#include "moe_layer.h"  /* the general router, the alignment of given ids, the dense int8 product */
+
 #endif /* QMOE_MOE_H */

@@ -24,6 +24,10 @@ MOE_Q_INT4_PER_CHANNEL, MOE_Q_MXFP8_COLWISE = 4, 5
 MOE_W_ROWMAJOR, MOE_W_TILED, MOE_W_FRAG = 0, 1, 2
 MOE_ACT_SWIGLU, MOE_ACT_SRELU = 0, 1
 MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_SLOTS = 128, 8, 65536
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_MAX_ROUTE_EXPERTS, MOE_MAX_ROUTE_GROUPS, MOE_MAX_INT8_K = 512, 64, 131071
 
 EXPORTS = [
     "moe_last_error", "moe_last_hip_error", "moe_align_max_padded", "moe_recommended_block_m",
@@ -35,6 +39,12 @@ EXPORTS = [
     "moe_grouped_gemm_int8w8a8", "moe_grouped_gemm_fp8w8a16", "moe_grouped_gemm_int4w4a16",
     "moe_grouped_gemm_int8w8a16", "moe_grouped_gemm_mxfp8", "moe_combine",
     "moe_quantize_act_colwise", "moe_grouped_gemm_mxfp8_wgrad",
+]
+
+# declared in include/moe_layer.h (which moe.h includes)
+LAYER_EXPORTS = [
+    "moe_route_topk", "moe_route_topk_backward", "moe_align_workspace_bytes",
+    "moe_align_topk_ids", "moe_gemm_int8w8a8_workspace_bytes", "moe_gemm_int8w8a8",
 ]
 
 
@@ -52,6 +62,8 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 _SIGS = {
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_last_hip_error": (_I, []),
@@ -75,6 +87,12 @@ _SIGS = {
     "moe_grouped_gemm_mxfp8_wgrad": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "moe_grouped_gemm_mxfp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_combine": (_I, [_P, _I, _I, _I, _P, _P]),
+    "moe_route_topk": (_I, [_P, _I, _L, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "moe_route_topk_backward": (_I, [_P, _P, _P, _I, _L, _I, _I, _I, _I, _I, _F, _P, _L, _P]),
+    "moe_align_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_align_topk_ids": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_gemm_int8w8a8_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_gemm_int8w8a8": (_I, [_P, _L, _P, _P, _L, _P, _P, _P, _I, _I, _I, _I, _P, _L, _P, _P]),
 }
 
 
@@ -107,6 +125,36 @@ def _stream(stream):
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
     return torch.cuda.current_stream().cuda_stream
+
+
+def _enqueue(name, tensors, args, stream):
+    """Call `name` with the arguments `args` makes of the device pointers of
+    `tensors` (None: an optional one left out), on `stream` or the current
+    stream of the tensors' device, with that device current.  Tensors on the
+    host or on different devices are refused; plain integer addresses are
+    taken as they are."""
+    import torch
+    dev = None
+    ptrs = []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if d < 0 or d != dev:
+            raise MoeError(MOE_EINVAL, f"{name}: tensors must be on one GPU, got {t.device}")
+        ptrs.append(t.data_ptr())
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    f = getattr(_lib or lib(), name)
+    if dev is not None and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _check(f(*args(*ptrs), stream))
+    return _check(f(*args(*ptrs), stream))
 
 
 def _check(rc):
@@ -247,3 +295,44 @@ def moe_grouped_gemm_mxfp8(a_q, a_sf, w_q, w_sf, m_offsets, rows, K, N, E, out, 
 
 def moe_combine(y, M, N, top_k, out, stream=None):
     return _check(lib().moe_combine(_ptr(y), M, N, top_k, _ptr(out), _stream(stream)))
+
+
+# ---- the layer around the grouped GEMMs ------------------------------------------
+def moe_route_topk(logits, dtype, ld, bias, M, E, top_k, score, n_group, topk_group, group_rule,
+                   renormalize, scale, topk_ids, topk_weights, stream=None):
+    return _enqueue(
+        "moe_route_topk", (logits, bias, topk_ids, topk_weights),
+        lambda x, b, i, w: (x, dtype, ld, b, M, E, top_k, score, n_group, topk_group, group_rule,
+                            renormalize, scale, i, w), stream)
+
+
+def moe_route_topk_backward(d_weights, topk_ids, logits, dtype, ld, M, E, top_k, score,
+                            renormalize, scale, d_logits, ldd, stream=None):
+    return _enqueue(
+        "moe_route_topk_backward", (d_weights, topk_ids, logits, d_logits),
+        lambda g, i, x, d: (g, i, x, dtype, ld, M, E, top_k, score, renormalize, scale, d, ldd),
+        stream)
+
+
+def moe_align_workspace_bytes(M, E, top_k):
+    return int(lib().moe_align_workspace_bytes(M, E, top_k))
+
+
+def moe_align_topk_ids(topk_ids, M, E, top_k, block_m, expert_first, sorted_token_ids, expert_ids,
+                       num_tokens_post_padded, expert_counts, workspace, stream=None):
+    return _enqueue(
+        "moe_align_topk_ids", (topk_ids, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                               expert_counts, workspace),
+        lambda i, s, e, n, c, w: (i, M, E, top_k, block_m, expert_first, s, e, n, c, w), stream)
+
+
+def moe_gemm_int8w8a8_workspace_bytes(M, K, N):
+    return int(lib().moe_gemm_int8w8a8_workspace_bytes(M, K, N))
+
+
+def moe_gemm_int8w8a8(a_q, lda, a_scale, w_q, ldw, w_scale, bias, addend, M, K, N, out_dtype, out,
+                      ldo, workspace, stream=None):
+    return _enqueue(
+        "moe_gemm_int8w8a8", (a_q, a_scale, w_q, w_scale, bias, addend, out, workspace),
+        lambda a, sa, w, sw, b, c, o, ws: (a, lda, sa, w, ldw, sw, b, c, M, K, N, out_dtype, o,
+                                           ldo, ws), stream)

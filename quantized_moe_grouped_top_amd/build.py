@@ -14,7 +14,7 @@ OUT = os.path.join(HERE, "libqmoe.so")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.normpath(os.path.join(HERE, "..", "include"))      # moe.h, the C ABI
 SOURCES = ["qmoe_api.cpp", "qmoe_align.hip", "qmoe_quant.hip", "qmoe_gemm.hip", "qmoe_gemm_tile.hip",
-           "qmoe_combine.hip"]
+           "qmoe_combine.hip", "qmoe_layer_api.cpp", "qmoe_route.hip", "qmoe_int8.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

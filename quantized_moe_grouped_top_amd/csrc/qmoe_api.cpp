@@ -9,14 +9,16 @@
 #include <mutex>
 
 #include "qmoe_internal.h"
+#include "qmoe_status.h"
 
 namespace {
 
-// MXFP8 row counts: rows plus the per-expert padding stay within int.
-constexpr int kMxMaxRows = 1 << 30;
-
 thread_local char g_err[512] = "";
 thread_local int g_hip_err = 0;
+
+}  // namespace
+
+namespace qmoe {
 
 int fail(int code, const char *fmt, ...) {
   va_list ap;
@@ -38,15 +40,6 @@ int hip_status(hipError_t e, const char *what) {
   return fail(MOE_EHIP, "%s: launch failed: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool valid_block_m(int b) { return b == 16 || b == 32 || b == 64 || b == 128 || b == 256; }
-
-#define REQUIRE(cond, code, ...)                  \
-  do {                                            \
-    if (!(cond)) return fail((code), __VA_ARGS__); \
-  } while (0)
-
 int check_routing_sizes(int M, int E, int top_k, const char *fn) {
   REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, MOE_EINVAL, "%s: E=%d outside [1, %d]", fn, E,
           MOE_MAX_EXPERTS);
@@ -63,6 +56,15 @@ long long max_padded_ll(int M, int E, int top_k, int block_m) {
   const long long n = (long long)M * top_k + (long long)E * (block_m - 1);
   return (n + block_m - 1) / block_m * block_m;
 }
+
+}  // namespace qmoe
+
+using namespace qmoe;
+
+namespace {
+
+// MXFP8 row counts: rows plus the per-expert padding stay within int.
+constexpr int kMxMaxRows = 1 << 30;
 
 // Outputs written by 32-bit buffer offsets (the out-of-range offset of the
 // tile GEMM's dropped stores lies above this)

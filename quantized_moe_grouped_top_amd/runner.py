@@ -12,23 +12,34 @@ current stream:
                      and MOE_Q_MXFP8_COLWISE weights; weight gradient =
                      moe_quantize_act_colwise (dy, x) -> moe_grouped_gemm_mxfp8_wgrad
     activation     : moe_act_quantize (SwiGLU / SReLU + MXFP8 or fp8)
+    general router : moe_route_topk -> moe_align_topk_ids in place of
+                     moe_align_block_size; its gradient moe_route_topk_backward
+    dense int8     : moe_quantize_act (int8 per token) -> moe_gemm_int8w8a8, e.g.
+                     a shared expert added to the routed experts' sum
 
 Every step runs in the library's HIP kernels; nothing here computes.
 """
 
 import torch
 
-from . import (MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_Q_FP8_PER_CHANNEL, MOE_Q_FP8_PER_TENSOR,
+from . import (MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F16, MOE_F32, MOE_GROUP_MAX,
+               MOE_GROUP_TOP2, MOE_Q_FP8_PER_CHANNEL, MOE_Q_FP8_PER_TENSOR,
                MOE_Q_INT4_PER_CHANNEL, MOE_Q_INT8_PER_CHANNEL, MOE_Q_MXFP8, MOE_Q_MXFP8_COLWISE,
-               MOE_W_FRAG,
+               MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_FRAG,
                MOE_W_ROWMAJOR,
-               MOE_W_TILED, moe_act_quantize, moe_align_block_size, moe_align_max_padded, moe_combine,
+               MOE_W_TILED, moe_act_quantize, moe_align_block_size, moe_align_max_padded,
+               moe_align_topk_ids, moe_align_workspace_bytes, moe_combine, moe_gemm_int8w8a8,
+               moe_gemm_int8w8a8_workspace_bytes,
                moe_grouped_gemm_fp8w8a8, moe_grouped_gemm_fp8w8a16, moe_grouped_gemm_int4w4a16,
                moe_grouped_gemm_int8w8a8,
                moe_grouped_gemm_int8w8a16,
                moe_grouped_gemm_mxfp8, moe_grouped_gemm_mxfp8_wgrad, moe_quantize_act_colwise,
                moe_mx_scale_rows, moe_pack_weights, moe_packed_weight_bytes, moe_quantize_act,
-               moe_quantize_weights, moe_quantize_workspace_bytes, moe_recommended_block_m)
+               moe_quantize_weights, moe_quantize_workspace_bytes, moe_recommended_block_m,
+               moe_route_topk, moe_route_topk_backward)
+
+_DTYPES = {"f32": (MOE_F32, torch.float32), "bf16": (MOE_BF16, torch.bfloat16),
+           "f16": (MOE_F16, torch.float16)}
 
 
 def _empty(shape, dtype, device):
@@ -83,13 +94,87 @@ def pack_weights(w_q, layout=MOE_W_TILED):
     return out
 
 
+class TopKRouter:
+    """General router of fixed (M, E, top_k): softmax or sigmoid scores, an
+    optional balance bias, groups, renormalised weights.  `route` fills
+    topk_ids / topk_weights; `align` groups the slots of the local experts
+    [expert_first, expert_first + n_local) for the grouped GEMMs and leaves
+    their loads in expert_counts; `backward` gives the logits' gradient."""
+
+    def __init__(self, M, E, top_k, dtype="f32", score="softmax", n_group=1, topk_group=1,
+                 group_rule="max", renormalize=True, scale=1.0, expert_first=0, n_local=None,
+                 device="cuda"):
+        self.M, self.E, self.top_k = M, E, top_k
+        self.dtype, self.torch_dtype = _DTYPES[dtype]
+        self.score = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score]
+        self.n_group, self.topk_group = n_group, topk_group
+        self.group_rule = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}[group_rule]
+        self.renormalize, self.scale = renormalize, scale
+        self.expert_first, self.n_local = expert_first, E if n_local is None else n_local
+        self.topk_ids = _empty((M, top_k), torch.int32, device)
+        self.topk_weights = _empty((M, top_k), torch.float32, device)
+        self.expert_counts = _empty((self.n_local,), torch.int32, device)
+        self.d_logits = _empty((M, E), self.torch_dtype, device)
+        self.ws = _empty((moe_align_workspace_bytes(M, self.n_local, top_k),), torch.uint8, device)
+
+    def route(self, logits, bias=None):
+        assert logits.dtype == self.torch_dtype and logits.shape == (self.M, self.E)
+        assert logits.stride(1) == 1
+        moe_route_topk(logits, self.dtype, logits.stride(0), bias, self.M, self.E, self.top_k,
+                       self.score, self.n_group, self.topk_group, self.group_rule,
+                       self.renormalize, self.scale, self.topk_ids, self.topk_weights)
+
+    def align(self, block_m, sorted_token_ids, expert_ids, num_tokens_post_padded):
+        moe_align_topk_ids(self.topk_ids, self.M, self.n_local, self.top_k, block_m,
+                           self.expert_first, sorted_token_ids, expert_ids,
+                           num_tokens_post_padded, self.expert_counts, self.ws)
+
+    def backward(self, d_weights, logits):
+        """d_logits [M, E] for d_weights [M, top_k], the choice held fixed."""
+        assert logits.dtype == self.torch_dtype and logits.stride(1) == 1
+        moe_route_topk_backward(d_weights, self.topk_ids, logits, self.dtype, logits.stride(0),
+                                self.M, self.E, self.top_k, self.score, self.renormalize,
+                                self.scale, self.d_logits, self.E)
+        return self.d_logits
+
+
+class Int8Linear:
+    """Dense int8 W8A8 linear of fixed (M, K, N): bf16 rows quantized per token,
+    int8 weights [N, K] with a scale per channel, an optional float32 bias and
+    an optional addend of the output's type (which may be the output)."""
+
+    def __init__(self, M, K, N, out="bf16", device="cuda"):
+        self.M, self.K, self.N = M, K, N
+        self.dtype, torch_dtype = _DTYPES[out]
+        self.a_q = _empty((M, K), torch.int8, device)
+        self.a_scale = _empty((max(M, 1),), torch.float32, device)
+        self.ws = _empty((moe_gemm_int8w8a8_workspace_bytes(M, K, N),), torch.uint8, device)
+        self.out = _empty((M, N), torch_dtype, device)
+
+    def quantize(self, x):
+        moe_quantize_act(x, self.M, self.K, MOE_Q_INT8_PER_CHANNEL, None, 1, self.a_q,
+                         self.a_scale, None, None)
+
+    def gemm(self, w_q, w_scale, bias=None, addend=None, out=None):
+        out = self.out if out is None else out
+        moe_gemm_int8w8a8(self.a_q, self.K, self.a_scale, w_q, w_q.stride(0), w_scale, bias, addend,
+                          self.M, self.K, self.N, self.dtype, out, self.N, self.ws)
+        return out
+
+    def forward(self, x, w_q, w_scale, bias=None, addend=None, out=None):
+        self.quantize(x)
+        return self.gemm(w_q, w_scale, bias, addend, out)
+
+
 class RoutedMoE:
     """fp8 W8A8, int8 W8A16 ("int8"), int8 W8A8 with per-token activation
     scales ("int8dq"), bf16 x fp8 weight-only ("fp8wo") or bf16 x int4
-    weight-only ("int4wo", block_m 16) MoE layer of fixed (M, K, N, E, top_k)."""
+    weight-only ("int4wo", block_m 16) MoE layer of fixed (M, K, N, E, top_k).
+    Tokens are routed by the fused softmax routing, or by `router` (a
+    TopKRouter of the same M and top_k whose local experts are the E here)."""
 
     def __init__(self, fmt, M, K, N, E, top_k, device="cuda", block_m=None,
-                 w_layout=MOE_W_ROWMAJOR):
+                 w_layout=MOE_W_ROWMAJOR, router=None):
         assert fmt in ("fp8", "int8", "int8dq", "fp8wo", "int4wo")
         self.w_layout = w_layout
         self.fmt, self.M, self.K, self.N, self.E, self.top_k = fmt, M, K, N, E, top_k
@@ -97,8 +182,13 @@ class RoutedMoE:
         self.max_padded = moe_align_max_padded(M, E, top_k, self.block_m)
         dev = device
         S = M * top_k
-        self.topk_ids = _empty((M, top_k), torch.int32, dev)
-        self.topk_weights = _empty((M, top_k), torch.float32, dev)
+        self.router = router
+        if router is not None:
+            assert (router.M, router.n_local, router.top_k) == (M, E, top_k)
+            self.topk_ids, self.topk_weights = router.topk_ids, router.topk_weights
+        else:
+            self.topk_ids = _empty((M, top_k), torch.int32, dev)
+            self.topk_weights = _empty((M, top_k), torch.float32, dev)
         self.sorted_token_ids = _empty((self.max_padded,), torch.int32, dev)
         self.expert_ids = _empty((self.max_padded // self.block_m,), torch.int32, dev)
         self.num_tokens_post_padded = _empty((1,), torch.int32, dev)
@@ -113,7 +203,15 @@ class RoutedMoE:
         self.y = _empty((S, N), torch.int16, dev)      # bf16 bits, one row per slot
         self.out = _empty((M, N), torch.int16, dev)     # bf16 bits
 
-    def route(self, logits):
+    def route(self, logits, bias=None):
+        if self.router is not None:
+            self.router.route(logits, bias)
+            self.router.align(self.block_m, self.sorted_token_ids, self.expert_ids,
+                              self.num_tokens_post_padded)
+            if self.router.n_local < self.router.E:      # slots of experts elsewhere add nothing
+                self.y.zero_()
+            return
+        assert bias is None, "a balance bias needs a TopKRouter"
         moe_align_block_size(logits, self.M, self.E, self.top_k, self.block_m, self.topk_ids,
                              self.topk_weights, self.sorted_token_ids, self.expert_ids,
                              self.num_tokens_post_padded)
@@ -157,12 +255,17 @@ class RoutedMoE:
     def combine(self):
         moe_combine(self.y, self.M, self.N, self.top_k, self.out)
 
-    def forward(self, x, logits, w_q, w_scale):
-        """One pass of the hot path; returns the bf16 output bits [M, N] (int16)."""
-        self.route(logits)
+    def forward(self, x, logits, w_q, w_scale, bias=None, shared=None):
+        """One pass of the hot path; returns the bf16 output bits [M, N] (int16).
+        `bias`: the router's balance bias; `shared` = (Int8Linear, w_q, w_scale):
+        a shared expert whose product is added to the routed experts' sum."""
+        self.route(logits, bias)
         self.quantize(x)
         self.gemm(x, w_q, w_scale)
         self.combine()
+        if shared is not None:
+            linear, sh_q, sh_scale = shared
+            linear.forward(x, sh_q, sh_scale, addend=self.out, out=self.out)
         return self.out
 
 
