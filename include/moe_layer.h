@@ -35,6 +35,7 @@ extern "C" {
                                          takes MOE_MAX_EXPERTS of them: see expert_first
                                          of moe_align_topk_ids) */
 #define MOE_MAX_ROUTE_GROUPS  64      /* n_group */
+#define MOE_MAX_ROUTE_TOKENS  (1 << 26)  /* M of the router lies below (one launch) */
 #define MOE_MAX_INT8_K        131071  /* K of the int8 product: |sum| <= 128*128*K < 2^31 */
 
 /* ======================================================================== *
@@ -58,7 +59,7 @@ extern "C" {
  *
  * Keys that rest on scores are computed in float64 and hold about 2^-40: of
  * two keys nearer than that either may come first (equal logits with equal
- * biases are exactly equal).  Weights are computed in float64 and rounded
+ * biases are exactly equal); what groups count is rounded to 38 bits.  Weights are computed in float64 and rounded
  * once to float32.
  * A logit or bias of -inf masks an expert: it is chosen only where fewer than
  * top_k others are left, and a -inf logit has score 0 (in a token without any
@@ -75,7 +76,7 @@ extern "C" {
  * Limits: 1 <= E <= MOE_MAX_ROUTE_EXPERTS, 1 <= top_k <= min(E, MOE_MAX_TOPK),
  * n_group <= MOE_MAX_ROUTE_GROUPS divides E, 1 <= topk_group <= n_group,
  * topk_group * (E / n_group) >= top_k, MOE_GROUP_TOP2 with n_group > 1 needs
- * two experts in a group.  M = 0 is valid. */
+ * two experts in a group, 0 <= M < MOE_MAX_ROUTE_TOKENS. */
 int moe_route_topk(const void *logits, int dtype, long long ld, const float *bias, int M, int E,
                    int top_k, int score, int n_group, int topk_group, int group_rule,
                    int renormalize, float scale, int *topk_ids, float *topk_weights,

@@ -29,18 +29,19 @@ def _sigmoid(v):
         return 1.0 / (1.0 + np.exp(-v))
 
 
-def _before(a, i, b, j):
-    """Whether (value a, index i) precedes (b, j): NaN first, then the larger
-    value, on equal values the lower index."""
-    if np.isnan(a) or np.isnan(b):
-        if np.isnan(a) and np.isnan(b):
-            return i < j
-        return bool(np.isnan(a))
-    return a > b or (a == b and i < j)
+def _to_38_bits(v):
+    """v with 38 bits behind its leading one: sums that are equal in exact
+    arithmetic (sigmoid(x) + sigmoid(-x) = 1) are equal here too, where their
+    float64 evaluations differ in the last bit."""
+    if not np.isfinite(v):
+        return v
+    m, e = np.frexp(v)
+    return float(np.ldexp(np.rint(np.ldexp(m, 39)), int(e) - 39))
 
 
 def _ranked(values, indices):
-    """indices in the order of _before."""
+    """indices by value: NaN first, then the larger value, on equal values the
+    lower index."""
     nan = [i for i in indices if np.isnan(values[i])]
     rest = sorted((i for i in indices if not np.isnan(values[i])), key=lambda i: (-values[i], i))
     return nan + rest
@@ -65,7 +66,7 @@ def route_general(logits, bias, top_k, score=SOFTMAX, n_group=1, topk_group=1,
                 worth[g] = key[_ranked(key, mine)[0]]
             elif gs >= 2:
                 a, b = _ranked(biased, mine)[:2]
-                worth[g] = biased[a] + biased[b]
+                worth[g] = _to_38_bits(biased[a] + biased[b])
         kept = range(n_group) if topk_group == n_group else _ranked(worth, range(n_group))[:topk_group]
         pool = [e for g in kept for e in range(g * gs, (g + 1) * gs)]
         chosen = _ranked(key, pool)[:top_k]

@@ -19,6 +19,8 @@ int check_route(int dtype, long long ld, int M, int E, int top_k, int score, con
   REQUIRE(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_EINVAL,
           "%s: unknown score %d", fn, score);
   REQUIRE(M >= 0 && E >= 1, MOE_EINVAL, "%s: M=%d E=%d", fn, M, E);
+  REQUIRE(M < MOE_MAX_ROUTE_TOKENS, MOE_EUNSUPPORTED, "%s: M=%d above %d", fn, M,
+          MOE_MAX_ROUTE_TOKENS - 1);
   REQUIRE(E <= MOE_MAX_ROUTE_EXPERTS, MOE_EUNSUPPORTED, "%s: E=%d above %d", fn, E,
           MOE_MAX_ROUTE_EXPERTS);
   REQUIRE(top_k >= 1 && top_k <= E, MOE_EINVAL, "%s: top_k=%d outside [1, E=%d]", fn, top_k, E);

@@ -6,175 +6,576 @@ namespace qmoe {
 
 namespace {
 
-// ---- router -------------------------------------------------------------------
-// Keys as 64-bit integers in the order of the doubles: NaN above every number,
-// -0 equal to +0.
-__device__ __forceinline__ uint64_t ordered(double v) {
-  if (v != v) return ~0ull;
-  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-  return (b >> 63) ? ~b : (b | (1ull << 63));
+// ---- rows of logits spread over lanes -------------------------------------------
+// G neighbouring lanes share a token; lane i of them holds the experts i*V ..
+// i*V + V - 1 in registers.
+
+// V values of a row from element e0 on as float32; elements at or past E read 0.
+// `vec`: rows and base are 16-byte aligned and V divides E, so a lane's values
+// exist all or not at all and load as whole words.
+template <int V>
+__device__ __forceinline__ void load_values(const void *base, long long row_at, int dtype, bool vec,
+                                            int e0, int E, float (&v)[V]) {
+#pragma unroll
+  for (int u = 0; u < V; ++u) v[u] = 0.0f;
+  if (dtype == MOE_F32) {
+    const float *x = (const float *)base + row_at + e0;
+    if constexpr (V % 4 == 0) {
+      if (vec) {
+        if (e0 < E) {
+#pragma unroll
+          for (int u = 0; u < V; u += 4) {
+            const f32x4 q = *reinterpret_cast<const f32x4 *>(x + u);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[u + c] = q[c];
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (e0 + u < E) v[u] = x[u];
+    return;
+  }
+  const uint16_t *x = (const uint16_t *)base + row_at + e0;
+  const bool bf = dtype == MOE_BF16;
+  if constexpr (V % 4 == 0) {
+    if (vec) {
+      if (e0 < E) {
+        constexpr int kW = V % 8 == 0 ? 4 : 2;             // dwords per load
+        typedef uint32_t words __attribute__((ext_vector_type(kW)));
+#pragma unroll
+        for (int u = 0; u < V; u += 2 * kW) {
+          const words q = *reinterpret_cast<const words *>(x + u);
+#pragma unroll
+          for (int c = 0; c < kW; ++c) {
+            v[u + 2 * c] = bf ? bf16_bits_to_f32(q[c] & 0xFFFFu) : TypeF16::load((uint16_t)q[c]);
+            v[u + 2 * c + 1] = bf ? bf16_bits_to_f32(q[c] >> 16) : TypeF16::load((uint16_t)(q[c] >> 16));
+          }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < V; ++u)
+    if (e0 + u < E) v[u] = bf ? bf16_bits_to_f32(x[u]) : TypeF16::load(x[u]);
+}
+
+// The value of the lane that a step of a G-lane reduction pairs this one with.
+// Step 0 and 1: the neighbours in a quad; 2: the other quad of 8 lanes; 3: the
+// other 8 of 16; 4 and 5: the other 16 of 32, the other 32 of 64.  After step
+// s all 2^(s+1) lanes hold the same, so mirrored lanes serve as partners.
+template <int kStep>
+__device__ __forceinline__ int lane_partner(int x) {
+  if constexpr (kStep == 0) return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);
+  else if constexpr (kStep == 1) return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);
+  else if constexpr (kStep == 2) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);
+  else if constexpr (kStep == 3) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false);
+  else return __shfl_xor(x, 1 << kStep);
+}
+template <int kStep>
+__device__ __forceinline__ float lane_partner(float x) {
+  return __int_as_float(lane_partner<kStep>(__float_as_int(x)));
+}
+template <int kStep>
+__device__ __forceinline__ double lane_partner(double x) {
+  const int lo = lane_partner<kStep>(__double2loint(x));
+  const int hi = lane_partner<kStep>(__double2hiint(x));
+  return __hiloint2double(hi, lo);
+}
+
+template <int G>
+struct Log2 {
+  static constexpr int value = 1 + Log2<G / 2>::value;
+};
+template <>
+struct Log2<1> {
+  static constexpr int value = 0;
+};
+template <int kStep, int kEnd, typename T>
+__device__ __forceinline__ T lanes_sum(T x) {
+  if constexpr (kStep < kEnd) return lanes_sum<kStep + 1, kEnd>(x + lane_partner<kStep>(x));
+  else return x;
+}
+template <int kStep, int kEnd>
+__device__ __forceinline__ float lanes_max(float x) {      // a NaN loses
+  if constexpr (kStep < kEnd) return lanes_max<kStep + 1, kEnd>(fmaxf(x, lane_partner<kStep>(x)));
+  else return x;
+}
+
+// ---- router: keys ------------------------------------------------------------------
+// A key is a double that carries its expert in the low 9 bits (so that its
+// order is that of (value, lower expert first) and one maximum instruction
+// compares both): what is below 2^-43 of a key's value is given up for it.
+// NaN keys and infinities are stood for by large finite values; -inf is
+// no key at all (an expert of a group that was left out, or none).
+constexpr int kIdBits = 9;
+constexpr int kIdMask = (1 << kIdBits) - 1;
+static_assert(MOE_MAX_ROUTE_EXPERTS == 1 << kIdBits, "a key holds its expert's number");
+
+__device__ __forceinline__ double stand_in_nan() { return __hiloint2double(0x7FEF0000, 0); }
+__device__ __forceinline__ double stand_in_inf() { return __hiloint2double(0x7FDF0000, 0); }
+
+// NaN and infinities replaced by their stand-ins
+__device__ __forceinline__ double finite(double k) {
+  const double c = stand_in_inf();
+  return k != k ? stand_in_nan() : k > c ? c : k < -c ? -c : k;
+}
+// and back
+__device__ __forceinline__ double unfinite(double k) {
+  const double c = stand_in_inf();
+  return k > c ? __builtin_nan("") : k == c ? INFINITY : k == -c ? -INFINITY : k;
+}
+
+template <int kBits>
+__device__ __forceinline__ double with_id(double k, int id) {
+  constexpr int kMask = (1 << kBits) - 1;
+  k += 0.0;                                                // -0 is +0
+  const int hi = __double2hiint(k), lo = __double2loint(k);
+  // below zero a larger magnitude is a smaller value
+  return __hiloint2double(hi, (lo & ~kMask) | ((id ^ ~(hi >> 31)) & kMask));
+}
+__device__ __forceinline__ int id_of(double k) {
+  return (__double2loint(k) ^ ~(__double2hiint(k) >> 31)) & kIdMask;
+}
+
+// 2^t for t <= 1000, about 2^-45 of the value: Chebyshev interpolation of
+// degree 9 on [-1/2, 1/2].
+__device__ __forceinline__ double exp2_poly(double t) {
+  const double n = __builtin_rint(t);
+  const double r = t - n;
+  double p = 1.0205905373362123e-07;
+  p = fma(p, r, 1.3259645246593194e-06);
+  p = fma(p, r, 1.525267292505434e-05);
+  p = fma(p, r, 0.0001540343375123525);
+  p = fma(p, r, 0.0013333558200794313);
+  p = fma(p, r, 0.009618129193934349);
+  p = fma(p, r, 0.05550410866465167);
+  p = fma(p, r, 0.2402265069564034);
+  p = fma(p, r, 0.6931471805599462);
+  p = fma(p, r, 1.0000000000000135);
+  return ldexp(p, (int)n);
+}
+constexpr double kLog2e = 1.4426950408889634;
+
+// 1 / (1 + exp(-x)) to about 2^-42 (absolute): beyond |x| = 80 the score is 0
+// or 1 within 2^-115, and 1 + exp(80) is still a float32, whose hardware
+// reciprocal starts one Newton step.
+__device__ __forceinline__ double sigmoid_key(float x) {
+  const float c = __builtin_amdgcn_fmed3f(x, -80.0f, 80.0f);
+  const double d = 1.0 + exp2_poly(-kLog2e * (double)c);
+  const double y = (double)__builtin_amdgcn_rcpf((float)d);
+  return fma(y, fma(-d, y, 1.0), y);
 }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-// One token per thread; keys are computed again wherever they are needed.
-template <typename Ty>
-__global__ __launch_bounds__(64) void route_topk_kernel(const RouteArgs a) {
-  const int t = blockIdx.x * 64 + threadIdx.x;
-  if (t >= a.M) return;
-  const typename Ty::T *x = (const typename Ty::T *)a.logits + (long long)t * a.ld;
-  const int E = a.E;
+// ---- router: sorted lists ------------------------------------------------------------
+__device__ __forceinline__ void exchange(double &a, double &b) {   // a >= b afterwards
+  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  a = hi;
+  b = lo;
+}
+// the larger KK of two descending lists, descending: the maxima of opposite
+// places form a bitonic sequence
+template <int KK>
+__device__ __forceinline__ void merge_lists(double (&a)[KK], const double (&b)[KK]) {
+#pragma unroll
+  for (int i = 0; i < KK; ++i) a[i] = __builtin_fmax(a[i], b[KK - 1 - i]);
+#pragma unroll
+  for (int d = KK / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < KK; ++i)
+      if ((i & d) == 0) exchange(a[i], a[i + d]);
+}
+template <int KK, int kStep, int kEnd>
+__device__ __forceinline__ void merge_lanes(double (&a)[KK]) {
+  if constexpr (kStep < kEnd) {
+    double b[KK];
+#pragma unroll
+    for (int i = 0; i < KK; ++i) b[i] = lane_partner<kStep>(a[i]);
+    merge_lists<KK>(a, b);
+    merge_lanes<KK, kStep + 1, kEnd>(a);
+  }
+}
+// 8 values, descending (a network of 19 exchanges)
+__device__ __forceinline__ void sort8(double (&a)[8]) {
+#define QMOE_X(i, j) exchange(a[i], a[j]);
+  QMOE_X(0, 2) QMOE_X(1, 3) QMOE_X(4, 6) QMOE_X(5, 7)
+  QMOE_X(0, 4) QMOE_X(1, 5) QMOE_X(2, 6) QMOE_X(3, 7)
+  QMOE_X(0, 1) QMOE_X(2, 3) QMOE_X(4, 5) QMOE_X(6, 7)
+  QMOE_X(2, 4) QMOE_X(3, 5)
+  QMOE_X(1, 4) QMOE_X(3, 6)
+  QMOE_X(1, 2) QMOE_X(3, 4) QMOE_X(5, 6)
+#undef QMOE_X
+}
+// the KK largest of a lane's V keys, descending, -inf where there are fewer
+template <int V, int KK>
+__device__ __forceinline__ void local_list(const double (&key)[V], double (&a)[KK]) {
+  if constexpr (KK == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = i < V ? key[i < V ? i : 0] : -INFINITY;
+    if constexpr (V > 1) sort8(a);
+#pragma unroll
+    for (int q = 8; q < V; q += 8) {
+      double b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = key[q + i];
+      sort8(b);
+      merge_lists<8>(a, b);
+    }
+  } else {
+    static_assert(KK == 2, "lists of 2 or 8");
+    a[0] = key[0];
+    a[1] = -INFINITY;
+#pragma unroll
+    for (int i = 1; i < V; ++i) {
+      a[1] = __builtin_fmax(a[1], __builtin_fmin(a[0], key[i]));
+      a[0] = __builtin_fmax(a[0], key[i]);
+    }
+  }
+}
+
+// the two largest of a lane's values joined over 2^n lanes
+template <int kStep, int kEnd>
+__device__ __forceinline__ void top2_lanes(double &m1, double &m2, int steps) {
+  if constexpr (kStep < kEnd) {
+    if (kStep < steps) {
+      const double o1 = lane_partner<kStep>(m1), o2 = lane_partner<kStep>(m2);
+      m2 = __builtin_fmax(__builtin_fmin(m1, o1), __builtin_fmax(m2, o2));
+      m1 = __builtin_fmax(m1, o1);
+      top2_lanes<kStep + 1, kEnd>(m1, m2, steps);
+    }
+  }
+}
+
+// What groups are ranked by, with the group's number in the low 6 bits.  It is
+// rounded to 38 bits first: sums that are equal in exact arithmetic, as
+// sigmoid(x) + sigmoid(-x) = 1 for every x, then tie in spite of the last bits
+// of their scores.
+static_assert(MOE_MAX_ROUTE_GROUPS == 64, "a group's worth holds its number");
+__device__ __forceinline__ double group_worth(double m1, double m2, bool top2, int g) {
+  const double w = top2 ? finite(unfinite(m1) + unfinite(m2)) : m1;
+  const long long bits = __double_as_longlong(w + 0.0);
+  return with_id<6>(__longlong_as_double((bits + 0x2000) & ~0x3FFFll), g);
+}
+
+enum { kNoGroups = 0, kLaneGroups = 1, kAnyGroups = 2 };
+
+// One token per G lanes.  The scores that keys rest on are computed in float64
+// by a polynomial; every lane sorts its V keys, and log2(G) merges of sorted
+// lists of KK leave the token's choice in every lane.  Groups: kLaneGroups
+// where a group is 2^n whole lanes, joined by lane steps; kAnyGroups ranks them
+// through LDS.
+template <int G, int V, int KK, int kGroups>
+__global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int dtype, bool vec,
+                                                         int lane_bits) {
+  constexpr int kTokens = 256 / G, kSteps = Log2<G>::value;
+  constexpr int kGroupSlots = G * V < 64 ? G * V : 64;
+  __shared__ float s_x[kTokens][G * V];                    // logits, for the chosen ones' weights
+  __shared__ double s_key[kGroups == kAnyGroups ? kTokens : 1][kGroups == kAnyGroups ? G * V : 1];
+  __shared__ double s_worth[kGroups == kAnyGroups ? kTokens : 1]
+                           [kGroups == kAnyGroups ? kGroupSlots : 1];
+  __shared__ uint8_t s_keep[kGroups == kAnyGroups ? kTokens : 1]
+                           [kGroups == kAnyGroups ? kGroupSlots : 1];
+  const int i = threadIdx.x & (G - 1), tok = threadIdx.x / G;
+  const long long t = (long long)blockIdx.x * kTokens + tok;
+  const bool live = t < a.M;                               // the same for a token's lanes
+  const int E = a.E, e0 = i * V;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
-  double m = 0.0, z = 1.0;
+
+  float v[V];
+  load_values<V>(a.logits, (live ? t : 0) * a.ld, dtype, vec, e0, E, v);
+#pragma unroll
+  for (int u = 0; u < V; ++u) s_x[tok][e0 + u] = v[u];
+
+  // ---- scores, where keys or groups rest on them
+  const bool top2 = kGroups != kNoGroups && a.group_rule == MOE_GROUP_TOP2;
+  const bool plain_softmax = soft && !a.renormalize;       // its weights need the whole sum
+  const bool scored = a.bias != nullptr || top2;
+  float m = -INFINITY;
+  double z = 0.0;
+  double key[V], sc[V];
+  bool odd = false;                                        // NaN or infinities here
+#pragma unroll
+  for (int u = 0; u < V; ++u) odd |= !(__builtin_fabsf(v[u]) < INFINITY);
+  if (soft && (scored || plain_softmax)) {
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (e0 + u < E) m = fmaxf(m, v[u]);
+    m = lanes_max<0, kSteps>(m);
+    if (m == -INFINITY) m = 0.0f;                          // nothing above -inf: scores 0 (or NaN)
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const double d = kLog2e * ((double)v[u] - (double)m);
+      sc[u] = d < -1100.0 ? 0.0 : exp2_poly(d);            // (a NaN stays one)
+      if (e0 + u < E) z += sc[u];
+    }
+    z = lanes_sum<0, kSteps>(z);
+    const double inv = z == 0.0 ? 0.0 : 1.0 / z;
+#pragma unroll
+    for (int u = 0; u < V; ++u) sc[u] *= inv;
+  } else if (scored) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) sc[u] = sigmoid_key(v[u]);
+    if (__any(odd)) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) sc[u] = v[u] != v[u] ? (double)v[u] : sc[u];
+    }
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const float b = e0 + u < E ? a.bias[e0 + u] : 0.0f;
+      odd |= !(__builtin_fabsf(b) < INFINITY);
+      sc[u] += (double)b;
+      key[u] = sc[u];
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < V; ++u) key[u] = (double)v[u];
+  }
+  if (__any(odd)) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      key[u] = finite(key[u]);
+      if (top2) sc[u] = finite(sc[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < V; ++u) key[u] = e0 + u < E ? with_id<kIdBits>(key[u], e0 + u) : -INFINITY;
+
+  // ---- groups
+  if constexpr (kGroups == kLaneGroups) {
+    // lanes [g * 2^n, (g + 1) * 2^n) are group g
+    double m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const double w = top2 ? sc[u] : key[u];
+      if (e0 + u < E) {
+        m2 = __builtin_fmax(m2, __builtin_fmin(m1, w));
+        m1 = __builtin_fmax(m1, w);
+      }
+    }
+    top2_lanes<0, kSteps>(m1, m2, lane_bits);
+    const int g = i >> lane_bits;
+    double w = group_worth(m1, m2, top2, g);
+    if (e0 >= E) w = -INFINITY;
+    int before = 0;                                        // groups better than this one
+    for (int o = 1; o < (G >> lane_bits); ++o) {
+      const int from = (threadIdx.x & 63) ^ (o << lane_bits);
+      const double other = __hiloint2double(__shfl(__double2hiint(w), from),
+                                            __shfl(__double2loint(w), from));
+      before += other > w;
+    }
+    if (before >= a.topk_group) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) key[u] = -INFINITY;
+    }
+  } else if constexpr (kGroups == kAnyGroups) {
+    const int gs = E / a.n_group;
+#pragma unroll
+    for (int u = 0; u < V; ++u) s_key[tok][e0 + u] = top2 ? sc[u] : key[u];
+    __syncthreads();
+    for (int g = i; g < a.n_group; g += G) {
+      double m1 = s_key[tok][g * gs], m2 = -INFINITY;
+      for (int q = 1; q < gs; ++q) {
+        const double w = s_key[tok][g * gs + q];
+        m2 = __builtin_fmax(m2, __builtin_fmin(m1, w));
+        m1 = __builtin_fmax(m1, w);
+      }
+      s_worth[tok][g] = group_worth(m1, m2, top2, g);
+    }
+    __syncthreads();
+    for (int g = i; g < a.n_group; g += G) {
+      const double w = s_worth[tok][g];
+      int before = 0;
+      for (int o = 0; o < a.n_group; ++o) before += s_worth[tok][o] > w;
+      s_keep[tok][g] = before < a.topk_group;
+    }
+    __syncthreads();
+    int g = e0 / gs, left = gs - (e0 - g * gs);            // experts of group g from here on
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      if (e0 + u < E && !s_keep[tok][g]) key[u] = -INFINITY;
+      if (--left == 0) {
+        ++g;
+        left = gs;
+      }
+    }
+  }
+
+  // ---- choice: the KK largest keys, in every lane of the token
+  double best[KK];
+  local_list<V, KK>(key, best);
+  merge_lanes<KK, 0, kSteps>(best);
+  __syncthreads();
+
+  // ---- weights: lane j the j-th choice
+  double mine = best[0];
+#pragma unroll
+  for (int j = 1; j < KK; ++j) mine = i == j ? best[j] : mine;
+  const bool chosen = i < a.top_k;
+  const int id = chosen ? id_of(mine) : 0;
+  const float xj = s_x[tok][id];
+  double w;
   if (soft) {
-    m = -INFINITY;
-    for (int e = 0; e < E; ++e) m = fmax(m, (double)Ty::load(x[e]));
-    if (m == -INFINITY) m = 0.0;                    // no logit above -inf: scores 0 (or NaN)
-    z = 0.0;
-    for (int e = 0; e < E; ++e) z += exp((double)Ty::load(x[e]) - m);
-  }
-  auto score = [&](int e) -> double {
-    const double v = (double)Ty::load(x[e]);
-    if (!soft) return sigmoid64(v);
-    return z == 0.0 ? 0.0 : exp(v - m) / z;
-  };
-  auto biased = [&](int e) -> double {
-    return a.bias ? score(e) + (double)a.bias[e] : score(e);
-  };
-  auto key = [&](int e) -> uint64_t {
-    return ordered(a.bias ? biased(e) : (double)Ty::load(x[e]));
-  };
-  uint64_t groups = ~0ull;                         // groups that stay
-  const int gs = E / a.n_group;
-  if (a.topk_group < a.n_group) {
-    groups = 0;
-    for (int r = 0; r < a.topk_group; ++r) {
-      int best = -1;
-      uint64_t best_v = 0;
-      for (int g = 0; g < a.n_group; ++g) {
-        if (groups >> g & 1) continue;
-        uint64_t v;
-        if (a.group_rule == MOE_GROUP_MAX) {
-          v = 0;
-          for (int e = g * gs; e < (g + 1) * gs; ++e) v = max(v, key(e));
-        } else {
-          double b1 = biased(g * gs), b2 = -INFINITY;
-          bool first = true;
-          for (int e = g * gs; e < (g + 1) * gs; ++e) {
-            const double w = biased(e);
-            if (first) {
-              b1 = w;
-              first = false;
-            } else if (ordered(w) > ordered(b1)) {
-              b2 = b1;
-              b1 = w;
-            } else if (ordered(w) > ordered(b2)) {
-              b2 = w;
-            }
-          }
-          v = ordered(b1 + b2);
-        }
-        if (best < 0 || v > best_v) {
-          best = g;
-          best_v = v;
-        }
-      }
-      groups |= 1ull << best;
-    }
-  }
-  // the j-th choice is the first expert, in the order of (key descending,
-  // expert ascending), after the (j-1)-th
-  int ids[kMaxTopK];
-  uint64_t prev = ~0ull;
-  int prev_id = -1;
-  for (int j = 0; j < a.top_k; ++j) {
-    int best = -1;
-    uint64_t best_v = 0;
-    for (int e = 0; e < E; ++e) {
-      if (!(groups >> (e / gs) & 1)) continue;
-      const uint64_t v = key(e);
-      const bool after = j == 0 || v < prev || (v == prev && e > prev_id);
-      if (after && (best < 0 || v > best_v)) {
-        best = e;
-        best_v = v;
-      }
-    }
-    ids[j] = best;
-    prev = best_v;
-    prev_id = best;
-  }
-  double w[kMaxTopK], sum = 0.0, mc = -INFINITY;
-  for (int j = 0; j < a.top_k; ++j) mc = fmax(mc, (double)Ty::load(x[ids[j]]));
-  if (mc == -INFINITY) mc = 0.0;
-  for (int j = 0; j < a.top_k; ++j) {
-    if (soft && a.renormalize) {
-      w[j] = exp((double)Ty::load(x[ids[j]]) - mc);
+    if (a.renormalize) {
+      m = lanes_max<0, 3>(chosen ? xj : -INFINITY);
+      if (m == -INFINITY) m = 0.0f;
+      w = exp((double)xj - (double)m);
     } else {
-      w[j] = score(ids[j]);
+      w = z == 0.0 ? 0.0 : exp((double)xj - (double)m) / z;
     }
-    sum += w[j];
+  } else {
+    w = sigmoid64((double)xj);
   }
-  for (int j = 0; j < a.top_k; ++j) {
-    const double q = a.renormalize ? (sum == 0.0 ? 0.0 : w[j] / sum) : w[j];
-    a.ids[(long long)t * a.top_k + j] = ids[j];
-    a.weights[(long long)t * a.top_k + j] = (float)(q * (double)a.scale);
+  if (a.renormalize) {
+    const double sum = lanes_sum<0, 3>(chosen ? w : 0.0);
+    w = sum == 0.0 ? 0.0 : w / sum;
+  }
+  if (live && chosen) {
+    a.ids[t * a.top_k + i] = id;
+    a.weights[t * a.top_k + i] = (float)(w * (double)a.scale);
   }
 }
 
 // ---- gradient -----------------------------------------------------------------
-// One token per thread.
-template <typename Ty>
-__global__ __launch_bounds__(64) void route_backward_kernel(const RouteBwdArgs a) {
-  const int t = blockIdx.x * 64 + threadIdx.x;
-  if (t >= a.M) return;
-  const typename Ty::T *x = (const typename Ty::T *)a.logits + (long long)t * a.ld;
-  typename Ty::T *dx = (typename Ty::T *)a.dx + (long long)t * a.ldd;
-  const int *ids = a.ids + (long long)t * a.top_k;
-  const float *dw = a.dw + (long long)t * a.top_k;
-  const int E = a.E, k = a.top_k;
+// One token per G lanes.  Lane j takes the j-th choice and its share of the
+// sums; then every lane builds its V gradients by looking for its experts among
+// the choices (no two lanes write one expert, whatever the choices are).  The
+// plain softmax reads the whole row for its scores, the others only the chosen
+// logits.
+template <int V>
+__device__ __forceinline__ void store_values(void *base, long long row_at, int dtype, bool vec,
+                                             int e0, int E, const float (&v)[V]) {
+  if (dtype == MOE_F32) {
+    float *x = (float *)base + row_at + e0;
+    if constexpr (V % 4 == 0) {
+      if (vec) {
+        if (e0 < E) {
+#pragma unroll
+          for (int u = 0; u < V; u += 4)
+            *reinterpret_cast<f32x4 *>(x + u) = f32x4{v[u], v[u + 1], v[u + 2], v[u + 3]};
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (e0 + u < E) x[u] = v[u];
+    return;
+  }
+  uint16_t *x = (uint16_t *)base + row_at + e0;
+  const bool bf = dtype == MOE_BF16;
+  if constexpr (V % 4 == 0) {
+    if (vec) {
+      if (e0 < E) {
+        constexpr int kW = V % 8 == 0 ? 4 : 2;
+        typedef uint32_t words __attribute__((ext_vector_type(kW)));
+#pragma unroll
+        for (int u = 0; u < V; u += 2 * kW) {
+          words q;
+#pragma unroll
+          for (int c = 0; c < kW; ++c)
+            q[c] = bf ? f32x2_to_bf16x2(v[u + 2 * c], v[u + 2 * c + 1])
+                      : (uint32_t)TypeF16::store(v[u + 2 * c]) |
+                            ((uint32_t)TypeF16::store(v[u + 2 * c + 1]) << 16);
+          *reinterpret_cast<words *>(x + u) = q;
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < V; ++u)
+    if (e0 + u < E) x[u] = bf ? TypeBf16::store(v[u]) : TypeF16::store(v[u]);
+}
+
+template <int G, int V, bool kDense>
+__global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs a, int dtype,
+                                                             bool vec_in, bool vec_out) {
+  constexpr int kTokens = 256 / G, kSteps = Log2<G>::value;
+  const int i = threadIdx.x & (G - 1), tok = threadIdx.x / G;
+  const long long t = (long long)blockIdx.x * kTokens + tok;
+  const bool live = t < a.M;
+  const int E = a.E, e0 = i * V, k = a.top_k;
+  const long long row = live ? t : 0;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
-  double d[kMaxTopK];                               // gradient of every choice's logit
-  double m = -INFINITY, z = 0.0, u = 0.0;
-  if (soft && !a.renormalize) {
-    for (int e = 0; e < E; ++e) m = fmax(m, (double)Ty::load(x[e]));
-    if (m == -INFINITY) m = 0.0;
-    for (int e = 0; e < E; ++e) z += exp((double)Ty::load(x[e]) - m);
-  } else if (soft) {
-    for (int j = 0; j < k; ++j)
-      if ((unsigned)ids[j] < (unsigned)E) m = fmax(m, (double)Ty::load(x[ids[j]]));
-    if (m == -INFINITY) m = 0.0;
+  float p[V];
+  if constexpr (kDense) load_values<V>(a.logits, row * a.ld, dtype, vec_in, e0, E, p);
+  // lane j < top_k: the j-th choice
+  int id = -1;
+  float g = 0.0f, x = 0.0f;
+  if (i < k) {
+    id = a.ids[row * k + i];
+    g = a.dw[row * k + i];
   }
-  double sum = 0.0;
-  for (int j = 0; j < k; ++j) {
-    d[j] = 0.0;
-    if ((unsigned)ids[j] >= (unsigned)E) continue;
-    const double v = (double)Ty::load(x[ids[j]]);
-    d[j] = soft ? exp(v - m) : sigmoid64(v);
-    sum += d[j];
+  const bool valid = (unsigned)id < (unsigned)E;
+  if (!valid) id = -1;
+  if (valid) {
+    if (dtype == MOE_F32) x = ((const float *)a.logits)[row * a.ld + id];
+    else if (dtype == MOE_BF16) x = TypeBf16::load(((const uint16_t *)a.logits)[row * a.ld + id]);
+    else x = TypeF16::load(((const uint16_t *)a.logits)[row * a.ld + id]);
   }
-  if (soft && !a.renormalize) sum = z;
-  const double inv = sum != 0.0 ? 1.0 / sum : 0.0;
-  const bool ratio = soft || a.renormalize;         // shares of a sum
-  for (int j = 0; j < k; ++j) {
-    if ((unsigned)ids[j] < (unsigned)E && ratio) u += (double)dw[j] * (d[j] * inv);
+  float d = 0.0f, back = 0.0f;                      // the choice's gradient; scale * u
+  if constexpr (kDense) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (e0 + u < E) m = fmaxf(m, p[u]);
+    m = lanes_max<0, kSteps>(m);
+    if (m == -INFINITY) m = 0.0f;
+    float z = 0.0f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      p[u] = e0 + u < E ? expf(p[u] - m) : 0.0f;
+      z += p[u];
+    }
+    z = lanes_sum<0, kSteps>(z);
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+    for (int u = 0; u < V; ++u) p[u] *= inv;
+    const float pj = valid ? expf(x - m) * inv : 0.0f;
+    back = a.scale * lanes_sum<0, kSteps>(g * pj);
+    d = a.scale * g;
+  } else {
+    double s = 0.0, tail = 1.0;
+    if (soft) {
+      float m = lanes_max<0, 3>(valid ? x : -INFINITY);
+      if (m == -INFINITY) m = 0.0f;
+      if (valid) s = exp((double)x - (double)m);
+    } else if (valid) {
+      s = sigmoid64((double)x);
+      tail = 1.0 / (1.0 + exp((double)x));
+    }
+    double c = (double)g;
+    if (a.renormalize) {
+      const double sum = lanes_sum<0, 3>(s);
+      s = sum == 0.0 ? 0.0 : s / sum;
+      c -= lanes_sum<0, 3>((double)g * s);
+    }
+    d = (float)((double)a.scale * s * c * tail);
   }
-  for (int j = 0; j < k; ++j) {
-    if ((unsigned)ids[j] >= (unsigned)E) continue;
-    const double v = (double)Ty::load(x[ids[j]]);
-    const double s = ratio ? d[j] * inv : d[j];
-    const double tail = soft ? 1.0 : 1.0 / (1.0 + exp(v));
-    // plain softmax: the -u term of every expert is added below
-    const double g = (double)dw[j] - (ratio && !(soft && !a.renormalize) ? u : 0.0);
-    d[j] = (double)a.scale * s * g * tail;
+  float o[V];
+#pragma unroll
+  for (int u = 0; u < V; ++u) o[u] = 0.0f;
+  const int first = (threadIdx.x & 63) & ~(G - 1);
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    if (j >= k) break;
+    const int at = __shfl(id, first + j) - e0;
+    const float dj = __shfl(d, first + j);
+#pragma unroll
+    for (int u = 0; u < V; ++u) o[u] += at == u ? dj : 0.0f;
   }
-  for (int e = 0; e < E; ++e) {
-    double g = 0.0;
-    for (int j = 0; j < k; ++j)
-      if (ids[j] == e) g += d[j];
-    if (soft && !a.renormalize)
-      g -= (double)a.scale * u * (exp((double)Ty::load(x[e]) - m) * inv);
-    dx[e] = Ty::store((float)g);
+  if constexpr (kDense) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) o[u] = p[u] * (o[u] - back);
   }
+  if (live) store_values<V>(a.dx, row * a.ldd, dtype, vec_out, e0, E, o);
 }
 
 // ---- alignment ------------------------------------------------------------------
@@ -214,20 +615,69 @@ __global__ __launch_bounds__(kMaxExperts) void align_ids_kernel(const AlignArgs 
 
 }  // namespace
 
-hipError_t launch_route_topk(const RouteArgs &a, int dtype, hipStream_t s) {
-  const dim3 g((unsigned)((a.M + 63) / 64)), b(64);
-  if (dtype == MOE_F32) hipLaunchKernelGGL(route_topk_kernel<TypeF32>, g, b, 0, s, a);
-  else if (dtype == MOE_BF16) hipLaunchKernelGGL(route_topk_kernel<TypeBf16>, g, b, 0, s, a);
-  else hipLaunchKernelGGL(route_topk_kernel<TypeF16>, g, b, 0, s, a);
+namespace {
+
+// Rows and base 16-byte aligned, and whole lanes of V values.
+bool vector_rows(const void *p, long long ld, int dtype, int E, int V) {
+  const long long bytes = ld * (dtype == MOE_F32 ? 4 : 2);
+  return ((uintptr_t)p & 15u) == 0 && bytes % 16 == 0 && E % V == 0;
+}
+
+template <int G, int V>
+hipError_t route_with(const RouteArgs &a, int dtype, hipStream_t s) {
+  const bool vec = vector_rows(a.logits, a.ld, dtype, a.E, V);
+  const long long blocks = ((long long)a.M * G + 255) / 256;
+  const dim3 grid((unsigned)blocks), block(256);
+  const int gs = a.E / a.n_group, lanes = gs / V;
+  const bool grouped = a.topk_group < a.n_group;
+  const bool by_lanes = gs % V == 0 && (lanes & (lanes - 1)) == 0;
+  int bits = 0;
+  while ((1 << bits) < lanes) ++bits;
+#define QMOE_ROUTE(kk, mode) \
+  hipLaunchKernelGGL((route_topk_kernel<G, V, kk, mode>), grid, block, 0, s, a, dtype, vec, bits)
+#define QMOE_ROUTE_K(mode)                 \
+  do {                                     \
+    if (a.top_k <= 2) QMOE_ROUTE(2, mode); \
+    else QMOE_ROUTE(8, mode);              \
+  } while (0)
+  if (!grouped) QMOE_ROUTE_K(kNoGroups);
+  else if (by_lanes) QMOE_ROUTE_K(kLaneGroups);
+  else QMOE_ROUTE_K(kAnyGroups);
+#undef QMOE_ROUTE_K
+#undef QMOE_ROUTE
   return hipGetLastError();
 }
 
-hipError_t launch_route_backward(const RouteBwdArgs &a, int dtype, hipStream_t s) {
-  const dim3 g((unsigned)((a.M + 63) / 64)), b(64);
-  if (dtype == MOE_F32) hipLaunchKernelGGL(route_backward_kernel<TypeF32>, g, b, 0, s, a);
-  else if (dtype == MOE_BF16) hipLaunchKernelGGL(route_backward_kernel<TypeBf16>, g, b, 0, s, a);
-  else hipLaunchKernelGGL(route_backward_kernel<TypeF16>, g, b, 0, s, a);
+template <int G, int V>
+hipError_t backward_with(const RouteBwdArgs &a, int dtype, hipStream_t s) {
+  const bool vin = vector_rows(a.logits, a.ld, dtype, a.E, V);
+  const bool vout = vector_rows(a.dx, a.ldd, dtype, a.E, V);
+  const dim3 grid((unsigned)(((long long)a.M * G + 255) / 256)), block(256);
+  if (a.score == MOE_SCORE_SOFTMAX && !a.renormalize)
+    hipLaunchKernelGGL((route_backward_kernel<G, V, true>), grid, block, 0, s, a, dtype, vin, vout);
+  else
+    hipLaunchKernelGGL((route_backward_kernel<G, V, false>), grid, block, 0, s, a, dtype, vin, vout);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_topk(const RouteArgs &a, int dtype, hipStream_t s) {
+  if (a.E <= 8) return route_with<8, 1>(a, dtype, s);
+  if (a.E <= 32) return route_with<8, 4>(a, dtype, s);
+  if (a.E <= 64) return route_with<8, 8>(a, dtype, s);
+  if (a.E <= 128) return route_with<16, 8>(a, dtype, s);
+  if (a.E <= 256) return route_with<32, 8>(a, dtype, s);
+  return route_with<64, 8>(a, dtype, s);
+}
+
+hipError_t launch_route_backward(const RouteBwdArgs &a, int dtype, hipStream_t s) {
+  if (a.E <= 8) return backward_with<8, 1>(a, dtype, s);
+  if (a.E <= 32) return backward_with<8, 4>(a, dtype, s);
+  if (a.E <= 64) return backward_with<8, 8>(a, dtype, s);
+  if (a.E <= 128) return backward_with<16, 8>(a, dtype, s);
+  if (a.E <= 256) return backward_with<32, 8>(a, dtype, s);
+  return backward_with<64, 8>(a, dtype, s);
 }
 
 hipError_t launch_align_ids(const AlignArgs &a, hipStream_t s) {

@@ -206,6 +206,13 @@ def check_backward(x, dtype, ids, g, score, renorm, scale, pad=0):
     tol = (eps + 2.0 ** -23) * np.abs(ref) + tiny + 2.0 ** -48 * mag * k
     if score == 0 and not renorm:
         tol = tol + _dense_tol(xs, cs, gs, scale)
+    # an expert chosen more than once: its at most k shares, each at most 2 mag
+    # (a share is scale * s * (g - u) with s <= 1 and |u| <= max|g|), are rounded
+    # to float32 (half a step each) and added in float32 (half a step of the
+    # partial sum each): 2^-24 * (2 mag k + 2 mag k)
+    for t in range(M):
+        ids_t, n = np.unique(cs[t][(cs[t] >= 0) & (cs[t] < E)], return_counts=True)
+        tol[t, ids_t[n > 1]] += 2.0 ** -24 * 4 * mag * k
     bad = np.abs(got - ref) > tol
     assert not bad.any(), (np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3])
     outside = np.ones((M, E), bool)
