@@ -579,38 +579,212 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
 }
 
 // ---- alignment ------------------------------------------------------------------
-// One workgroup: thread e counts, places and labels the slots of expert e.
-__global__ __launch_bounds__(kMaxExperts) void align_ids_kernel(const AlignArgs a) {
-  __shared__ int s_cnt[kMaxExperts];
-  __shared__ int s_off[kMaxExperts + 1];
-  const int e = threadIdx.x;
-  int n = 0;
-  if (e < a.E) {
-    for (int i = 0; i < a.S; ++i) n += (long long)a.ids[i] - a.expert_first == e;
-    s_cnt[e] = n;
-    if (a.counts) a.counts[e] = n;
+// A stable counting sort of the slots by local expert.  Every wavefront owns a
+// run of slots; for 64 of them one ballot per bit of the expert's number gives
+// each lane the lanes with the same expert, so ranks need no atomics and keep
+// the slots' order.
+constexpr int kAlignThreads = 1024;
+constexpr int kAlignWaves = kAlignThreads / 64;
+constexpr int kOneWorkgroupChunks = 4;          // up to here one workgroup is as fast as many
+constexpr int kChunk = 1024;                     // slots of one workgroup where there are many
+
+// local expert of a slot, or -1
+__device__ __forceinline__ int local_expert(int id, int first, int E) {
+  return id >= first && (unsigned)id - (unsigned)first < (unsigned)E ? (int)((unsigned)id - (unsigned)first)
+                                                                     : -1;
+}
+
+__device__ __forceinline__ unsigned long long peers_of(int e, int nbits) {
+  unsigned long long peers = __ballot(e >= 0);
+  for (int b = 0; b < nbits; ++b) {
+    const bool bit = (e >> b) & 1;
+    const unsigned long long mb = __ballot(bit);
+    peers &= bit ? mb : ~mb;
   }
-  __syncthreads();
-  if (e == 0) {
-    int at = 0;
-    for (int q = 0; q < a.E; ++q) {
-      s_off[q] = at;
-      at += (s_cnt[q] + a.block_m - 1) / a.block_m * a.block_m;
+  return peers;
+}
+__device__ __forceinline__ int lanes_below(unsigned long long mask) {
+  return __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0u));
+}
+
+// Exclusive scan of the padded group sizes by wavefront 0: lane l holds the
+// experts l and l + 64.  Fills s_off[0 .. E].
+__device__ __forceinline__ void padded_starts(const int *s_cnt, int E, int block_m, int *s_off) {
+  const int lane = threadIdx.x;
+  const int n0 = lane < E ? s_cnt[lane] : 0, n1 = lane + 64 < E ? s_cnt[lane + 64] : 0;
+  const int c0 = (n0 + block_m - 1) & -block_m, c1 = (n1 + block_m - 1) & -block_m;  // a power of two
+  int x0 = c0, x1 = c1;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y0 = __shfl_up(x0, d), y1 = __shfl_up(x1, d);
+    if (lane >= d) {
+      x0 += y0;
+      x1 += y1;
     }
-    s_off[a.E] = at;
-    *a.num_post = at;
+  }
+  const int half = __shfl(x0, 63);
+  if (lane < E) s_off[lane] = x0 - c0;
+  if (lane + 64 < E) s_off[lane + 64] = half + x1 - c1;
+  if (lane == 0) s_off[E] = 0;
+  const int total = half + __shfl(x1, 63);
+  if (lane == 0) s_off[E] = total;
+}
+
+// Everything that is not a slot: block labels, padding, the tail, counts; the
+// `part`-th of `parts` workgroups does its share.
+__device__ __forceinline__ void align_rest(const AlignArgs &a, const int *s_off, const int *s_cnt,
+                                           int part, int parts) {
+  const int tid = threadIdx.x, total = s_off[a.E];
+  const int step = parts * kAlignThreads, at = part * kAlignThreads + tid;
+  for (int b = at; b < a.max_padded / a.block_m; b += step) {
+    const int p = b * a.block_m;
+    int label = -1;
+    if (p < total) {
+      int lo = 0, hi = a.E - 1;                  // the last expert that starts at or before p
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_off[mid] <= p) lo = mid;
+        else hi = mid - 1;
+      }
+      label = lo;
+    }
+    a.expert_ids[b] = label;
+  }
+  for (int e = part * kAlignWaves + (tid >> 6); e < a.E; e += parts * kAlignWaves)
+    for (int p = s_off[e] + s_cnt[e] + (tid & 63); p < s_off[e + 1]; p += 64) a.sorted_ids[p] = a.S;
+  for (int p = total + at; p < a.max_padded; p += step) a.sorted_ids[p] = a.S;
+  if (part == 0) {
+    if (a.counts && tid < a.E) a.counts[tid] = s_cnt[tid];
+    if (tid == 0) *a.num_post = total;
+  }
+}
+
+// Slots [begin, end) of one workgroup, wavefront w its w-th run of `per` (a
+// multiple of 64): the counts of every wavefront and expert ...
+__device__ __forceinline__ void count_slots(const AlignArgs &a, int begin, int end, int per, int nbits,
+                                            int (*s_wave)[kMaxExperts]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lo = begin + wave * per, hi = min(lo + per, end);
+  for (int base = lo; base < hi; base += 64) {
+    const int e = base + lane < hi ? local_expert(a.ids[base + lane], a.expert_first, a.E) : -1;
+    const unsigned long long peers = peers_of(e, nbits);
+    if (e >= 0 && lanes_below(peers) == 0) s_wave[wave][e] += __popcll(peers);
+  }
+}
+// ... and their places, s_wave holding each wavefront's next place per expert.
+__device__ __forceinline__ void place_slots(const AlignArgs &a, int begin, int end, int per, int nbits,
+                                            int (*s_wave)[kMaxExperts]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lo = begin + wave * per, hi = min(lo + per, end);
+  for (int base = lo; base < hi; base += 64) {
+    const int e = base + lane < hi ? local_expert(a.ids[base + lane], a.expert_first, a.E) : -1;
+    const unsigned long long peers = peers_of(e, nbits);
+    if (e >= 0) {
+      const int rank = lanes_below(peers), at = s_wave[wave][e];   // read by every lane first ...
+      a.sorted_ids[at + rank] = base + lane;
+      if (rank == 0) s_wave[wave][e] = at + __popcll(peers);       // ... then written by one
+    }
+  }
+}
+
+__device__ __forceinline__ int bits_for(int E) { return E > 1 ? 32 - __builtin_clz((unsigned)(E - 1)) : 0; }
+
+// Few slots: one workgroup does it all.
+__global__ __launch_bounds__(kAlignThreads) void align_one_kernel(const AlignArgs a) {
+  __shared__ int s_wave[kAlignWaves][kMaxExperts];
+  __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts + 1];
+  const int tid = threadIdx.x, nbits = bits_for(a.E);
+  const int per = ((a.S + kAlignWaves - 1) / kAlignWaves + 63) & ~63;
+  for (int x = tid; x < kAlignWaves * kMaxExperts; x += kAlignThreads) (&s_wave[0][0])[x] = 0;
+  __syncthreads();
+  count_slots(a, 0, a.S, per, nbits, s_wave);
+  __syncthreads();
+  if (tid < a.E) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kAlignWaves; ++w) n += s_wave[w][tid];
+    s_cnt[tid] = n;
   }
   __syncthreads();
-  if (e < a.E) {
-    int p = s_off[e];
-    for (int b = p; b < s_off[e + 1]; b += a.block_m) a.expert_ids[b / a.block_m] = e;
-    for (int i = 0; i < a.S; ++i)
-      if ((long long)a.ids[i] - a.expert_first == e) a.sorted_ids[p++] = i;
-    for (; p < s_off[e + 1]; ++p) a.sorted_ids[p] = a.S;
+  if (tid < 64) padded_starts(s_cnt, a.E, a.block_m, s_off);
+  __syncthreads();
+  if (tid < a.E) {
+    int at = s_off[tid];
+#pragma unroll
+    for (int w = 0; w < kAlignWaves; ++w) {
+      const int n = s_wave[w][tid];
+      s_wave[w][tid] = at;
+      at += n;
+    }
   }
-  for (int p = s_off[a.E] + e; p < a.max_padded; p += blockDim.x) a.sorted_ids[p] = a.S;
-  for (int b = s_off[a.E] / a.block_m + e; b < a.max_padded / a.block_m; b += blockDim.x)
-    a.expert_ids[b] = -1;
+  __syncthreads();
+  place_slots(a, 0, a.S, per, nbits, s_wave);
+  align_rest(a, s_off, s_cnt, 0, 1);
+}
+
+// Many slots: workgroup b counts chunk b into ws[b], [E] each ...
+__global__ __launch_bounds__(kAlignThreads) void align_count_kernel(const AlignArgs a) {
+  __shared__ int s_wave[kAlignWaves][kMaxExperts];
+  const int tid = threadIdx.x, begin = blockIdx.x * kChunk;
+  for (int x = tid; x < kAlignWaves * kMaxExperts; x += kAlignThreads) (&s_wave[0][0])[x] = 0;
+  __syncthreads();
+  count_slots(a, begin, min(begin + kChunk, a.S), 64, bits_for(a.E), s_wave);
+  __syncthreads();
+  if (tid < a.E) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kAlignWaves; ++w) n += s_wave[w][tid];
+    a.ws[blockIdx.x * a.E + tid] = n;
+  }
+}
+
+// ... and, from the counts of all chunks, places its own.
+__global__ __launch_bounds__(kAlignThreads) void align_place_kernel(const AlignArgs a) {
+  constexpr int kParts = kAlignThreads / kMaxExperts;
+  __shared__ int s_wave[kAlignWaves][kMaxExperts];
+  __shared__ int s_all[kParts][kMaxExperts], s_pre[kParts][kMaxExperts];
+  __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts + 1];
+  const int tid = threadIdx.x, begin = blockIdx.x * kChunk, nbits = bits_for(a.E);
+  for (int x = tid; x < kAlignWaves * kMaxExperts; x += kAlignThreads) (&s_wave[0][0])[x] = 0;
+  // slots of an expert in all chunks and in those before this one: every
+  // kParts-th chunk by one group of kMaxExperts threads
+  const int e = tid % kMaxExperts, part = tid / kMaxExperts, chunks = gridDim.x;
+  int all = 0, pre = 0;
+  if (e < a.E) {
+    for (int c = part; c < chunks; c += kParts) {
+      const int n = a.ws[c * a.E + e];
+      all += n;
+      pre += c < (int)blockIdx.x ? n : 0;
+    }
+  }
+  s_all[part][e] = all;
+  s_pre[part][e] = pre;
+  __syncthreads();
+  count_slots(a, begin, min(begin + kChunk, a.S), 64, nbits, s_wave);
+  if (tid < a.E) {
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) n += s_all[q][tid];
+    s_cnt[tid] = n;
+  }
+  __syncthreads();
+  if (tid < 64) padded_starts(s_cnt, a.E, a.block_m, s_off);
+  __syncthreads();
+  if (tid < a.E) {
+    int at = s_off[tid];
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) at += s_pre[q][tid];
+#pragma unroll
+    for (int w = 0; w < kAlignWaves; ++w) {
+      const int n = s_wave[w][tid];
+      s_wave[w][tid] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  place_slots(a, begin, min(begin + kChunk, a.S), 64, nbits, s_wave);
+  align_rest(a, s_off, s_cnt, blockIdx.x, chunks);
 }
 
 }  // namespace
@@ -681,7 +855,16 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, int dtype, hipStream_t s
 }
 
 hipError_t launch_align_ids(const AlignArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(align_ids_kernel, dim3(1), dim3(kMaxExperts), 0, s, a);
+  const int chunks = (a.S + kChunk - 1) / kChunk;
+  const dim3 b(kAlignThreads);
+  if (chunks <= kOneWorkgroupChunks) {
+    hipLaunchKernelGGL(align_one_kernel, dim3(1), b, 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(align_count_kernel, dim3(chunks), b, 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(align_place_kernel, dim3(chunks), b, 0, s, a);
   return hipGetLastError();
 }
 
