@@ -1,6 +1,7 @@
 // Dense int8 product with a scale per token and per output channel:
 //   out[m, n] = round((sum_k a[m,k] w[n,k]) * a_scale[m] * w_scale[n] + bias[n] + addend[m, n])
 // The sums are exact: int8 products added in int32 on the int8 MFMA.
+#include "qmoe_device.h"
 #include "qmoe_layer.h"
 
 namespace qmoe {
@@ -73,16 +74,387 @@ __global__ __launch_bounds__(256) void int8_any_kernel(const Int8Args p) {
   }
 }
 
+// Sixteen columns of one row, held as eight values in each of the lanes l and
+// l + 32 (values 0-3: columns 4 g .., 4-7: columns 8 + 4 g .. of the run; g = the
+// lane's half): scales, bias and addend in float32, then 16-byte stores of
+// eight columns a lane for the 16-bit types (one swap between the lane halves
+// a register pair), 4 columns a lane for float32.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef int i32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef int i32x2u __attribute__((ext_vector_type(2), aligned(2)));
+template <typename Ty>
+__device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int col, int g, float sa,
+                                          const float *s_sw, const float *s_bias, const i32x16 &acc,
+                                          int v0) {
+  typedef typename Ty::T T;
+  constexpr bool kWide = sizeof(T) == 4;
+  const bool row_ok = m < p.M;
+  const long long row = (long long)m * p.ldo;
+  const bool whole = n0 + col + 16 <= p.N;             // the same in every lane
+  float f[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4 sw = *reinterpret_cast<const f32x4 *>(s_sw + col + 8 * h + 4 * g);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[4 * h + c] = (float)acc[v0 + 4 * h + c] * sa * sw[c];
+    if (p.bias) {
+      const f32x4 b = *reinterpret_cast<const f32x4 *>(s_bias + col + 8 * h + 4 * g);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f[4 * h + c] += b[c];
+    }
+    if (p.addend && row_ok) {
+      const T *add = (const T *)p.addend + row + n0 + col + 8 * h + 4 * g;
+      if (whole) {
+        T v[4];
+        if constexpr (kWide) {
+          const f32x4u q = *reinterpret_cast<const f32x4u *>(add);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = q[c];
+        } else {
+          const i32x2u q = *reinterpret_cast<const i32x2u *>(add);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = (T)(q[c >> 1] >> (16 * (c & 1)));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[4 * h + c] += Ty::load(v[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n0 + col + 8 * h + 4 * g + c < p.N) f[4 * h + c] += Ty::load(add[c]);
+      }
+    }
+  }
+  T *out = (T *)p.out + row + n0;
+  if constexpr (kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = col + 8 * h + 4 * g;
+      if (!row_ok) continue;
+      if (whole) {
+        *reinterpret_cast<f32x4u *>(out + at) = f32x4{f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n0 + at + c < p.N) out[at + c] = f[4 * h + c];
+      }
+    }
+  } else {
+    int x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = Ty::pack(f[2 * q], f[2 * q + 1]);
+    if (whole) {
+      const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+      if (row_ok)
+        *reinterpret_cast<i32x4u *>(out + col + 8 * g) =
+            i32x4{(int)s0[0], (int)s1[0], (int)s0[1], (int)s1[1]};
+    } else if (row_ok) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int at = col + 8 * (c >> 2) + 4 * g + (c & 3);
+        if (n0 + at < p.N) out[at] = (T)(x[c >> 1] >> (16 * (c & 1)));
+      }
+    }
+  }
+}
+
+// ---- many rows: 256 x 256 tiles ---------------------------------------------------
+// One workgroup of eight wavefronts per CU, two on each SIMD; wavefront (wm, wn)
+// owns 128 rows x 64 columns in 128 accumulation registers.  128 bytes of k of
+// the tile's 512 rows (64 KB) come by direct-to-LDS DMA into one of two slots.
+//
+// The wavefronts of the upper and the lower half of the rows work in opposite
+// phase: while one half reads the fragments of 64 k from LDS, the other
+// multiplies the 64 k that it read in the phase before, so that every SIMD's
+// matrix unit has one of its two wavefronts' products to do at any time.  A
+// barrier ends each phase.  A slot is free once the lower half has read its
+// second 64 k; the next-but-one stage's DMA is issued right then and has four
+// phases to land.
+constexpr int kBM = 256, kBN = 256, kBK = 128;
+constexpr int kBigThreads = 512;
+constexpr int kBigA = kBM * kBK;                     // bytes of activations in a slot
+constexpr int kBigSlot = (kBM + kBN) * kBK;
+
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void phase_end() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tile t of an XCD-aware order: the tiles are cut into eight contiguous runs,
+// one for each XCD; inside, four row tiles go together, rows fastest, so the
+// 32 tiles that an XCD works on at a time are 4 x 8.
+struct TileOrder {
+  int ntm, ntn;
+  __device__ __forceinline__ void at(int t, int &tm, int &tn) const {
+    constexpr int kRows = 4;
+    const int per = kRows * ntn, g = t / per, rem = t - g * per;
+    const int rows = min(kRows, ntm - g * kRows);
+    tn = rem / rows;
+    tm = g * kRows + rem - tn * rows;
+  }
+};
+
+#define QMOE_INLINE __attribute__((always_inline))
+
+template <typename Ty>
+__global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args p, TileOrder order) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kBigSlot];
+  __shared__ float s_sa[kBM], s_sw[kBN], s_bias[kBN];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = wave >> 2, wn = wave & 3;          // rows 128 half .., columns 64 wn ..
+  const int g = lane >> 5, r32 = lane & 31;
+  const int full = p.K / kBK;                         // whole stages
+  const int tail = p.K - full * kBK;
+
+  // this workgroup's tiles: those of its XCD's run, round robin
+  const int total = order.ntm * order.ntn;
+  const int G = gridDim.x, b = blockIdx.x;
+  const int xcd = b & (kXcds - 1), wl = b / kXcds;
+  const int gx = (G - xcd + kXcds - 1) / kXcds;
+  const int run = (total + kXcds - 1) / kXcds;
+  const int t_end = min((xcd + 1) * run, total);
+
+  const uint32_t ring = lds_addr(s_ring);
+  // fragment addresses of this lane: row part and the four chunks of a stage
+  const int sw = swz(r32);
+  uint32_t a_rd[4], w_rd[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {                       // c = 2 * (64-k half) + (32-k half of it)
+    const uint32_t ch = (uint32_t)(((2 * c + g) ^ sw) << 4);
+    a_rd[c] = (uint32_t)((half * 128 + r32) * kBK) + ch;
+    w_rd[c] = (uint32_t)(kBigA + (wn * 64 + r32) * kBK) + ch;
+  }
+
+  const int8_t *a_src = nullptr, *w_src = nullptr;
+  uint32_t a_off[4], w_off[4];
+  int m0 = 0, n0 = 0;
+  // offsets of this lane's DMA pieces: wavefront w copies rows 32 w .. 32 w + 31
+  // of both operands, 8 rows an instruction
+  auto enter = [&](int t) QMOE_INLINE {
+    int tm, tn;
+    order.at(t, tm, tn);
+    m0 = tm * kBM;
+    n0 = tn * kBN;
+    a_src = p.a + (long long)m0 * p.lda;
+    w_src = p.w + (long long)n0 * p.ldw;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = 32 * wave + 8 * u + (lane >> 3);
+      const uint32_t ch = 16u * (uint32_t)((lane & 7) ^ swz(r));
+      a_off[u] = (uint32_t)min(r, p.M - 1 - m0) * (uint32_t)p.lda + ch;
+      w_off[u] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.ldw + ch;
+    }
+  };
+  auto dma_piece = [&](int s, int slot) QMOE_INLINE {
+    const uint32_t at = ring + (uint32_t)(slot * kBigSlot + wave * 4096);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dma16(a_src + s * kBK, a_off[u], at + u * 1024);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dma16(w_src + s * kBK, w_off[u], at + kBigA + u * 1024);
+  };
+
+  i32x16 acc[4][2];
+  i32x4 fa[4][2], fw[2][2];
+  auto read_half = [&](int slot, int h) QMOE_INLINE {
+    const uint8_t *base = s_ring + slot * kBigSlot;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        fw[j][c] = *reinterpret_cast<const i32x4 *>(base + w_rd[2 * h + c] + j * 32 * kBK);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        fa[i][c] = *reinterpret_cast<const i32x4 *>(base + a_rd[2 * h + c] + i * 32 * kBK);
+    }
+  };
+  auto multiply = [&]() QMOE_INLINE {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+  };
+
+  int t = xcd * run + wl;
+  if (t >= t_end) return;
+  enter(t);
+  int first = 0;                                      // slot of this tile's stage 0
+  if (full > 0) {
+    dma_piece(0, 0);
+    wait_dma_all();                                   // stage 0 has landed here ...
+  }
+  phase_end();                                        // ... and everywhere
+  for (;;) {
+    const int cm0 = m0, cn0 = n0;
+    const bool more = t + gx < t_end;
+    // this wavefront's part of stage d; stage `full` is the next tile's first
+    auto dma_stage = [&](int d) QMOE_INLINE {
+      if (d < full) {
+        dma_piece(d, (first + d) & 1);
+      } else if (d == full && more) {
+        enter(t + gx);
+        dma_piece(0, (first + d) & 1);
+      }
+    };
+    // scales and bias of this tile, on their way while it is computed
+    float side = 0.0f, side2 = 0.0f;
+    if (tid < kBN) {
+      side = p.w_scale[min(cn0 + tid, p.N - 1)];
+      if (p.bias) side2 = p.bias[min(cn0 + tid, p.N - 1)];
+    } else {
+      side = p.a_scale[min(cm0 + tid - kBN, p.M - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+    if (full > 0) {
+      if (half == 0) {
+        for (int s = 0; s < full; ++s) {
+          const int slot = (first + s) & 1;
+          dma_stage(s + 1);
+          read_half(slot, 0);
+          wait_lds();
+          phase_end();
+          __builtin_amdgcn_s_setprio(1);
+          multiply();
+          __builtin_amdgcn_s_setprio(0);
+          phase_end();
+          read_half(slot, 1);
+          wait_lds();
+          phase_end();
+          __builtin_amdgcn_s_setprio(1);
+          multiply();
+          __builtin_amdgcn_s_setprio(0);
+          wait_dma_all();                             // stage s + 1 has landed here
+          phase_end();
+        }
+        phase_end();
+      } else {
+        dma_stage(1);
+        phase_end();
+        for (int s = 0; s < full; ++s) {
+          const int slot = (first + s) & 1;
+          read_half(slot, 0);
+          wait_lds();
+          phase_end();
+          __builtin_amdgcn_s_setprio(1);
+          multiply();
+          __builtin_amdgcn_s_setprio(0);
+          phase_end();
+          read_half(slot, 1);
+          wait_lds();
+          wait_dma_all();
+          phase_end();
+          dma_stage(s + 2);                           // the slot is free from here on
+          __builtin_amdgcn_s_setprio(1);
+          multiply();
+          __builtin_amdgcn_s_setprio(0);
+          phase_end();
+        }
+      }
+    }
+    first = (first + full) & 1;
+    if (tail > 0) {
+      // the rest of k, zero past K: 512 rows of 8 chunks, through registers into
+      // the slot that the next tile's first stage is not in
+      const int k0 = full * kBK, slot = first ^ 1;
+      const int8_t *ar = p.a + (long long)cm0 * p.lda, *wr = p.w + (long long)cn0 * p.ldw;
+#pragma unroll 1
+      for (int q = tid; q < (kBM + kBN) * 8; q += kBigThreads) {
+        const int r = (q >> 3) & (kBM - 1), c = q & 7;
+        const bool is_a = q < kBM * 8;
+        const int8_t *row = is_a ? ar + (long long)min(r, p.M - 1 - cm0) * p.lda
+                                 : wr + (long long)min(r, p.N - 1 - cn0) * p.ldw;
+        *reinterpret_cast<i32x4 *>(s_ring + slot * kBigSlot + (is_a ? 0 : kBigA) + r * kBK +
+                                   ((c ^ swz(r)) << 4)) = load16(row, k0 + 16 * c, p.K);
+      }
+      wait_lds();
+      phase_end();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        read_half(slot, h);
+        multiply();
+      }
+      wait_lds();
+      phase_end();
+    }
+    if (full == 0 && more) enter(t + gx);
+
+    if (tid < kBN) {
+      s_sw[tid] = side;
+      s_bias[tid] = side2;
+    } else {
+      s_sa[tid - kBN] = side;
+    }
+    wait_lds();
+    phase_end();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ml = half * 128 + 32 * i + r32;
+      const float sa = s_sa[ml];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          store_run<Ty>(p, cm0 + ml, cn0, wn * 64 + 32 * j + 16 * kk, g, sa, s_sw, s_bias, acc[i][j],
+                        8 * kk);
+    }
+    if (!more) break;
+    t += gx;
+  }
+}
+
 }  // namespace
 
 size_t int8_workspace_bytes(int, int, int) { return 0; }
 
-hipError_t launch_int8_gemm(const Int8Args &a, int out_dtype, hipStream_t s) {
+namespace {
+
+int compute_units() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+    n = 256;
+  return n;
+}
+
+template <typename Ty>
+hipError_t launch(const Int8Args &a, hipStream_t s) {
+  // rows that direct-to-LDS copies can take
+  const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
+                       a.ldw % 16 == 0;
+  if (aligned && a.M > 256) {
+    const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};
+    const long long tiles = (long long)order.ntm * order.ntn;
+    const int cus = compute_units();
+    hipLaunchKernelGGL(int8_big_kernel<Ty>, dim3((unsigned)(tiles < cus ? tiles : cus)),
+                       dim3(kBigThreads), 0, s, a, order);
+    return hipGetLastError();
+  }
   const dim3 g((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64)), b(256);
-  if (out_dtype == MOE_F32) hipLaunchKernelGGL(int8_any_kernel<TypeF32>, g, b, 0, s, a);
-  else if (out_dtype == MOE_BF16) hipLaunchKernelGGL(int8_any_kernel<TypeBf16>, g, b, 0, s, a);
-  else hipLaunchKernelGGL(int8_any_kernel<TypeF16>, g, b, 0, s, a);
+  hipLaunchKernelGGL(int8_any_kernel<Ty>, g, b, 0, s, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_gemm(const Int8Args &a, int out_dtype, hipStream_t s) {
+  if (out_dtype == MOE_F32) return launch<TypeF32>(a, s);
+  if (out_dtype == MOE_BF16) return launch<TypeBf16>(a, s);
+  return launch<TypeF16>(a, s);
 }
 
 }  // namespace qmoe

@@ -20,6 +20,7 @@ struct TypeBf16 {
   typedef uint16_t T;
   static __device__ __forceinline__ float load(T v) { return bf16_bits_to_f32(v); }
   static __device__ __forceinline__ T store(float v) { return (T)f32x2_to_bf16x2(v, v); }
+  static __device__ __forceinline__ int pack(float a, float b) { return (int)f32x2_to_bf16x2(a, b); }
 };
 struct TypeF16 {
   typedef uint16_t T;
@@ -28,6 +29,9 @@ struct TypeF16 {
   }
   static __device__ __forceinline__ T store(float v) {
     return __builtin_bit_cast(uint16_t, __float2half_rn(v));
+  }
+  static __device__ __forceinline__ int pack(float a, float b) {
+    return (int)((uint32_t)store(a) | ((uint32_t)store(b) << 16));
   }
 };
 
