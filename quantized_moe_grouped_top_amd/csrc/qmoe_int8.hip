@@ -1,6 +1,8 @@
 // Dense int8 product with a scale per token and per output channel:
 //   out[m, n] = round((sum_k a[m,k] w[n,k]) * a_scale[m] * w_scale[n] + bias[n] + addend[m, n])
 // The sums are exact: int8 products added in int32 on the int8 MFMA.
+#include <type_traits>
+
 #include "qmoe_device.h"
 #include "qmoe_layer.h"
 
@@ -159,27 +161,37 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
 }
 
 // ---- many rows: 256 x 256 tiles ---------------------------------------------------
-// One workgroup of eight wavefronts per CU, two on each SIMD; wavefront (wm, wn)
-// owns 128 rows x 64 columns in 128 accumulation registers.  128 bytes of k of
-// the tile's 512 rows (64 KB) come by direct-to-LDS DMA into one of two slots.
+// One workgroup of eight wavefronts per CU, two on each SIMD; wavefront (half,
+// wn) owns 128 rows x 64 columns in 128 accumulation registers.  A stage is 64 k
+// of the tile's 512 rows (32 KB), copied by direct-to-LDS DMA into one of four
+// slots.
 //
 // The wavefronts of the upper and the lower half of the rows work in opposite
-// phase: while one half reads the fragments of 64 k from LDS, the other
-// multiplies the 64 k that it read in the phase before, so that every SIMD's
-// matrix unit has one of its two wavefronts' products to do at any time.  A
-// barrier ends each phase.  A slot is free once the lower half has read its
-// second 64 k; the next-but-one stage's DMA is issued right then and has four
-// phases to land.
-constexpr int kBM = 256, kBN = 256, kBK = 128;
+// phase: while one half reads a stage's fragments from LDS, the other multiplies
+// the stage that it read in the phase before, so that one of the two wavefronts
+// of every SIMD has products to do at any time.  A barrier ends each phase.  The
+// DMA of the stage three ahead goes out between the products, one copy every
+// four of them: issued in one go, the copies of a stage hold up their wavefronts
+// (128-k stages in two slots, all copies at once: 1900 cycles in that phase, 540
+// in the others, 244 us for 4096 x 14336 x 4096).
+constexpr int kBM = 256, kBN = 256, kBK = 64;
 constexpr int kBigThreads = 512;
+constexpr int kRing = 4;
 constexpr int kBigA = kBM * kBK;                     // bytes of activations in a slot
 constexpr int kBigSlot = (kBM + kBN) * kBK;
+constexpr int kBigPieces = 4;                        // copies of a wavefront and stage
 
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+// 16-byte chunk c of a 64-byte LDS row r lies at c ^ swz(r): the 16 rows that a
+// fragment read takes at a time lie on distinct banks
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 3)) & 3; }
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void wait_dma() {         // all but the last n have landed
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
 __device__ __forceinline__ void phase_end() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_barrier" ::: "memory");
@@ -204,7 +216,7 @@ struct TileOrder {
 
 template <typename Ty>
 __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args p, TileOrder order) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kBigSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kRing * kBigSlot];
   __shared__ float s_sa[kBM], s_sw[kBN], s_bias[kBN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -220,98 +232,110 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
   const int gx = (G - xcd + kXcds - 1) / kXcds;
   const int run = (total + kXcds - 1) / kXcds;
   const int t_end = min((xcd + 1) * run, total);
+  int t = xcd * run + wl;
+  if (t >= t_end) return;
 
   const uint32_t ring = lds_addr(s_ring);
-  // fragment addresses of this lane: row part and the four chunks of a stage
-  const int sw = swz(r32);
-  uint32_t a_rd[4], w_rd[4];
+  uint32_t a_rd[2], w_rd[2];                          // this lane's fragments of the two 32-k steps
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {                       // c = 2 * (64-k half) + (32-k half of it)
-    const uint32_t ch = (uint32_t)(((2 * c + g) ^ sw) << 4);
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t ch = (uint32_t)(((2 * c + g) ^ swz(r32)) << 4);
     a_rd[c] = (uint32_t)((half * 128 + r32) * kBK) + ch;
     w_rd[c] = (uint32_t)(kBigA + (wn * 64 + r32) * kBK) + ch;
   }
 
+  // ---- the copy cursor: stage cur_s of tile cur_t is the next to be copied.  When
+  // every stage is, the last is copied again into slots nobody reads, so that
+  // the counts of copies in flight stay the same.
+  int cur_t = t, cur_s = 0, cur_slot = 0;
   const int8_t *a_src = nullptr, *w_src = nullptr;
-  uint32_t a_off[4], w_off[4];
-  int m0 = 0, n0 = 0;
-  // offsets of this lane's DMA pieces: wavefront w copies rows 32 w .. 32 w + 31
-  // of both operands, 8 rows an instruction
-  auto enter = [&](int t) QMOE_INLINE {
+  uint32_t a_off[2], w_off[2];
+  auto enter = [&](int tt) QMOE_INLINE {
     int tm, tn;
-    order.at(t, tm, tn);
-    m0 = tm * kBM;
-    n0 = tn * kBN;
+    order.at(tt, tm, tn);
+    const int m0 = tm * kBM, n0 = tn * kBN;
     a_src = p.a + (long long)m0 * p.lda;
     w_src = p.w + (long long)n0 * p.ldw;
+    // wavefront w copies rows 32 w .. 32 w + 31 of both operands, 16 an instruction
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = 32 * wave + 8 * u + (lane >> 3);
-      const uint32_t ch = 16u * (uint32_t)((lane & 7) ^ swz(r));
+    for (int u = 0; u < 2; ++u) {
+      const int r = 32 * wave + 16 * u + (lane >> 2);
+      const uint32_t ch = 16u * (uint32_t)((lane & 3) ^ swz(r));
       a_off[u] = (uint32_t)min(r, p.M - 1 - m0) * (uint32_t)p.lda + ch;
       w_off[u] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.ldw + ch;
     }
   };
-  auto dma_piece = [&](int s, int slot) QMOE_INLINE {
-    const uint32_t at = ring + (uint32_t)(slot * kBigSlot + wave * 4096);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) dma16(a_src + s * kBK, a_off[u], at + u * 1024);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) dma16(w_src + s * kBK, w_off[u], at + kBigA + u * 1024);
+  auto dma_piece = [&](int u) QMOE_INLINE {
+    const uint32_t at = ring + (uint32_t)(cur_slot * kBigSlot + wave * 2048 + (u & 1) * 1024);
+    if (u < 2) dma16(a_src + cur_s * kBK, a_off[u], at);
+    else dma16(w_src + cur_s * kBK, w_off[u - 2], at + kBigA);
+  };
+  auto dma_next = [&]() QMOE_INLINE {                 // the cursor's stage is on its way
+    cur_slot = (cur_slot + 1) & (kRing - 1);
+    if (cur_s + 1 < full) {
+      ++cur_s;
+    } else if (cur_t + gx < t_end) {
+      cur_t += gx;
+      cur_s = 0;
+      enter(cur_t);
+    }
   };
 
   i32x16 acc[4][2];
   i32x4 fa[4][2], fw[2][2];
-  auto read_half = [&](int slot, int h) QMOE_INLINE {
+  auto read_stage = [&](int slot) QMOE_INLINE {
     const uint8_t *base = s_ring + slot * kBigSlot;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        fw[j][c] = *reinterpret_cast<const i32x4 *>(base + w_rd[2 * h + c] + j * 32 * kBK);
+        fw[j][c] = *reinterpret_cast<const i32x4 *>(base + w_rd[c] + j * 32 * kBK);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        fa[i][c] = *reinterpret_cast<const i32x4 *>(base + a_rd[2 * h + c] + i * 32 * kBK);
+        fa[i][c] = *reinterpret_cast<const i32x4 *>(base + a_rd[c] + i * 32 * kBK);
     }
   };
-  auto multiply = [&]() QMOE_INLINE {
+  // the products of a stage, with (kDma) the cursor's copies between them
+  auto multiply = [&](auto with_dma) QMOE_INLINE {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+    for (int q = 0; q < 16; ++q) {
+      const int c = q >> 3, j = (q >> 2) & 1, i = q & 3;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+      if constexpr (decltype(with_dma)::value) {
+        if ((q & 3) == 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          dma_piece(q >> 2);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
   };
 
-  int t = xcd * run + wl;
-  if (t >= t_end) return;
-  enter(t);
-  int first = 0;                                      // slot of this tile's stage 0
   if (full > 0) {
-    dma_piece(0, 0);
-    wait_dma_all();                                   // stage 0 has landed here ...
+    enter(t);
+#pragma unroll
+    for (int d = 0; d < kRing - 1; ++d) {
+#pragma unroll
+      for (int u = 0; u < kBigPieces; ++u) dma_piece(u);
+      dma_next();
+    }
+    wait_dma<2 * kBigPieces>();                       // stage 0 has landed here ...
   }
   phase_end();                                        // ... and everywhere
+  int slot = 0;                                       // of the stage being computed
   for (;;) {
-    const int cm0 = m0, cn0 = n0;
-    const bool more = t + gx < t_end;
-    // this wavefront's part of stage d; stage `full` is the next tile's first
-    auto dma_stage = [&](int d) QMOE_INLINE {
-      if (d < full) {
-        dma_piece(d, (first + d) & 1);
-      } else if (d == full && more) {
-        enter(t + gx);
-        dma_piece(0, (first + d) & 1);
-      }
-    };
+    int tm, tn;
+    order.at(t, tm, tn);
+    const int m0 = tm * kBM, n0 = tn * kBN;
     // scales and bias of this tile, on their way while it is computed
     float side = 0.0f, side2 = 0.0f;
     if (tid < kBN) {
-      side = p.w_scale[min(cn0 + tid, p.N - 1)];
-      if (p.bias) side2 = p.bias[min(cn0 + tid, p.N - 1)];
+      side = p.w_scale[min(n0 + tid, p.N - 1)];
+      if (p.bias) side2 = p.bias[min(n0 + tid, p.N - 1)];
     } else {
-      side = p.a_scale[min(cm0 + tid - kBN, p.M - 1)];
+      side = p.a_scale[min(m0 + tid - kBN, p.M - 1)];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -320,78 +344,57 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 
+    // Phase 2 s: the upper half reads stage s; phase 2 s + 1: the lower half
+    // does.  Stage s + 1 has to be there after phase 2 s + 1, when the upper half
+    // has issued the copies up to stage s + 3, the lower half up to s + 2.
     if (full > 0) {
       if (half == 0) {
         for (int s = 0; s < full; ++s) {
-          const int slot = (first + s) & 1;
-          dma_stage(s + 1);
-          read_half(slot, 0);
+          read_stage(slot);
           wait_lds();
           phase_end();
-          __builtin_amdgcn_s_setprio(1);
-          multiply();
-          __builtin_amdgcn_s_setprio(0);
+          multiply(std::true_type{});
+          dma_next();
+          wait_dma<2 * kBigPieces>();
           phase_end();
-          read_half(slot, 1);
-          wait_lds();
-          phase_end();
-          __builtin_amdgcn_s_setprio(1);
-          multiply();
-          __builtin_amdgcn_s_setprio(0);
-          wait_dma_all();                             // stage s + 1 has landed here
-          phase_end();
+          slot = (slot + 1) & (kRing - 1);
         }
         phase_end();
       } else {
-        dma_stage(1);
         phase_end();
         for (int s = 0; s < full; ++s) {
-          const int slot = (first + s) & 1;
-          read_half(slot, 0);
+          read_stage(slot);
           wait_lds();
+          wait_dma<kBigPieces>();
           phase_end();
-          __builtin_amdgcn_s_setprio(1);
-          multiply();
-          __builtin_amdgcn_s_setprio(0);
+          multiply(std::true_type{});
+          dma_next();
           phase_end();
-          read_half(slot, 1);
-          wait_lds();
-          wait_dma_all();
-          phase_end();
-          dma_stage(s + 2);                           // the slot is free from here on
-          __builtin_amdgcn_s_setprio(1);
-          multiply();
-          __builtin_amdgcn_s_setprio(0);
-          phase_end();
+          slot = (slot + 1) & (kRing - 1);
         }
       }
     }
-    first = (first + full) & 1;
     if (tail > 0) {
-      // the rest of k, zero past K: 512 rows of 8 chunks, through registers into
-      // the slot that the next tile's first stage is not in
-      const int k0 = full * kBK, slot = first ^ 1;
-      const int8_t *ar = p.a + (long long)cm0 * p.lda, *wr = p.w + (long long)cn0 * p.ldw;
+      // the rest of k, zero past K: 512 rows of 4 chunks, through registers into
+      // the slot of the last stage (the next three are being filled)
+      const int k0 = full * kBK, ts = (slot + kRing - 1) & (kRing - 1);
+      const int8_t *ar = p.a + (long long)m0 * p.lda, *wr = p.w + (long long)n0 * p.ldw;
 #pragma unroll 1
-      for (int q = tid; q < (kBM + kBN) * 8; q += kBigThreads) {
-        const int r = (q >> 3) & (kBM - 1), c = q & 7;
-        const bool is_a = q < kBM * 8;
-        const int8_t *row = is_a ? ar + (long long)min(r, p.M - 1 - cm0) * p.lda
-                                 : wr + (long long)min(r, p.N - 1 - cn0) * p.ldw;
-        *reinterpret_cast<i32x4 *>(s_ring + slot * kBigSlot + (is_a ? 0 : kBigA) + r * kBK +
+      for (int q = tid; q < (kBM + kBN) * 4; q += kBigThreads) {
+        const int r = (q >> 2) & (kBM - 1), c = q & 3;
+        const bool is_a = q < kBM * 4;
+        const int8_t *row = is_a ? ar + (long long)min(r, p.M - 1 - m0) * p.lda
+                                 : wr + (long long)min(r, p.N - 1 - n0) * p.ldw;
+        *reinterpret_cast<i32x4 *>(s_ring + ts * kBigSlot + (is_a ? 0 : kBigA) + r * kBK +
                                    ((c ^ swz(r)) << 4)) = load16(row, k0 + 16 * c, p.K);
       }
       wait_lds();
       phase_end();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        read_half(slot, h);
-        multiply();
-      }
+      read_stage(ts);
+      multiply(std::false_type{});
       wait_lds();
       phase_end();
     }
-    if (full == 0 && more) enter(t + gx);
 
     if (tid < kBN) {
       s_sw[tid] = side;
@@ -409,12 +412,13 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
-          store_run<Ty>(p, cm0 + ml, cn0, wn * 64 + 32 * j + 16 * kk, g, sa, s_sw, s_bias, acc[i][j],
+          store_run<Ty>(p, m0 + ml, n0, wn * 64 + 32 * j + 16 * kk, g, sa, s_sw, s_bias, acc[i][j],
                         8 * kk);
     }
-    if (!more) break;
     t += gx;
+    if (t >= t_end) break;
   }
+  wait_dma_all();                                     // no copy into LDS outlives the workgroup
 }
 
 }  // namespace
