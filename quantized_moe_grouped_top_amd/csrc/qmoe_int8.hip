@@ -183,7 +183,7 @@ constexpr int kBigPieces = 4;                        // copies of a wavefront an
 
 // 16-byte chunk c of a 64-byte LDS row r lies at c ^ swz(r): the 16 rows that a
 // fragment read takes at a time lie on distinct banks
-__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 3)) & 3; }
+__device__ __forceinline__ int swz(int r) { return (r >> 2) & 3; }
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
 }
