@@ -76,36 +76,38 @@ __global__ __launch_bounds__(256) void int8_any_kernel(const Int8Args p) {
   }
 }
 
-// Sixteen columns of one row, held as eight values in each of the lanes l and
-// l + 32 (values 0-3: columns 4 g .., 4-7: columns 8 + 4 g .. of the run; g = the
-// lane's half): scales, bias and addend in float32, then 16-byte stores of
-// eight columns a lane for the 16-bit types (one swap between the lane halves
-// a register pair), 4 columns a lane for float32.
+// 32 columns of one row, held in the lanes l, l + 16, l + 32, l + 48 (g = 0 .. 3):
+// four sums of columns 4 g .. 4 g + 3 of the first sixteen (lo) and of the second
+// (hi).  Scales, bias and addend in float32; then for float32 one 16-byte store
+// of each, for the 16-bit types one of eight neighbouring columns, after one swap
+// of odd and even groups of 16 lanes a register pair.  `col` is the run's first
+// column in the tile that starts at column n0.
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef int i32x4u __attribute__((ext_vector_type(4), aligned(2)));
 typedef int i32x2u __attribute__((ext_vector_type(2), aligned(2)));
 template <typename Ty>
 __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int col, int g, float sa,
-                                          const float *s_sw, const float *s_bias, const i32x16 &acc,
-                                          int v0) {
+                                          const float *s_sw, const float *s_bias, const i32x4 &lo,
+                                          const i32x4 &hi) {
   typedef typename Ty::T T;
   constexpr bool kWide = sizeof(T) == 4;
   const bool row_ok = m < p.M;
   const long long row = (long long)m * p.ldo;
-  const bool whole = n0 + col + 16 <= p.N;             // the same in every lane
+  const bool whole = n0 + col + 32 <= p.N;             // the same in every lane
   float f[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const f32x4 sw = *reinterpret_cast<const f32x4 *>(s_sw + col + 8 * h + 4 * g);
+    const int at = col + 16 * h + 4 * g;
+    const f32x4 sw = *reinterpret_cast<const f32x4 *>(s_sw + at);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) f[4 * h + c] = (float)acc[v0 + 4 * h + c] * sa * sw[c];
+    for (int c = 0; c < 4; ++c) f[4 * h + c] = (float)(h ? hi[c] : lo[c]) * sa * sw[c];
     if (p.bias) {
-      const f32x4 b = *reinterpret_cast<const f32x4 *>(s_bias + col + 8 * h + 4 * g);
+      const f32x4 b = *reinterpret_cast<const f32x4 *>(s_bias + at);
 #pragma unroll
       for (int c = 0; c < 4; ++c) f[4 * h + c] += b[c];
     }
     if (p.addend && row_ok) {
-      const T *add = (const T *)p.addend + row + n0 + col + 8 * h + 4 * g;
+      const T *add = (const T *)p.addend + row + n0 + at;
       if (whole) {
         T v[4];
         if constexpr (kWide) {
@@ -122,7 +124,7 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (n0 + col + 8 * h + 4 * g + c < p.N) f[4 * h + c] += Ty::load(add[c]);
+          if (n0 + at + c < p.N) f[4 * h + c] += Ty::load(add[c]);
       }
     }
   }
@@ -130,7 +132,7 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
   if constexpr (kWide) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = col + 8 * h + 4 * g;
+      const int at = col + 16 * h + 4 * g;
       if (!row_ok) continue;
       if (whole) {
         *reinterpret_cast<f32x4u *>(out + at) = f32x4{f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
@@ -145,15 +147,16 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[q] = Ty::pack(f[2 * q], f[2 * q + 1]);
     if (whole) {
-      const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
-      const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+      // groups 0, 2: eight columns of the first sixteen; 1, 3: of the second
+      const auto s0 = __builtin_amdgcn_permlane16_swap(x[0], x[2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane16_swap(x[1], x[3], false, false);
       if (row_ok)
-        *reinterpret_cast<i32x4u *>(out + col + 8 * g) =
+        *reinterpret_cast<i32x4u *>(out + col + 16 * (g & 1) + 8 * (g >> 1)) =
             i32x4{(int)s0[0], (int)s1[0], (int)s0[1], (int)s1[1]};
     } else if (row_ok) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int at = col + 8 * (c >> 2) + 4 * g + (c & 3);
+        const int at = col + 16 * (c >> 2) + 4 * g + (c & 3);
         if (n0 + at < p.N) out[at] = (T)(x[c >> 1] >> (16 * (c & 1)));
       }
     }
@@ -164,7 +167,10 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
 // One workgroup of eight wavefronts per CU, two on each SIMD; wavefront (half,
 // wn) owns 128 rows x 64 columns in 128 accumulation registers.  A stage is 64 k
 // of the tile's 512 rows (32 KB), copied by direct-to-LDS DMA into one of four
-// slots.
+// slots.  The products are v_mfma_i32_16x16x64_i8: with 64 k in one instruction
+// it moves half the accumulator values a product that 32x32x32 does, and where
+// power sets the clock that counts (registers only, normally distributed codes:
+// 4030 TOP/s at 1.98 GHz against 3350 at 1.60 GHz).
 //
 // The wavefronts of the upper and the lower half of the rows work in opposite
 // phase: while one half reads a stage's fragments from LDS, the other multiplies
@@ -181,9 +187,9 @@ constexpr int kBigA = kBM * kBK;                     // bytes of activations in 
 constexpr int kBigSlot = (kBM + kBN) * kBK;
 constexpr int kBigPieces = 4;                        // copies of a wavefront and stage
 
-// 16-byte chunk c of a 64-byte LDS row r lies at c ^ swz(r): the 16 rows that a
-// fragment read takes at a time lie on distinct banks
-__device__ __forceinline__ int swz(int r) { return (r >> 2) & 3; }
+// 16-byte chunk c of a 64-byte LDS row r lies at c ^ swz(r): the lanes that a
+// fragment read serves at a time lie on distinct banks (counted: no conflicts)
+__device__ __forceinline__ int swz(int r) { return -(r >> 2) & 3; }
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
 }
@@ -221,7 +227,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = wave >> 2, wn = wave & 3;          // rows 128 half .., columns 64 wn ..
-  const int g = lane >> 5, r32 = lane & 31;
+  const int g = lane >> 4, r16 = lane & 15;
   const int full = p.K / kBK;                         // whole stages
   const int tail = p.K - full * kBK;
 
@@ -236,13 +242,10 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
   if (t >= t_end) return;
 
   const uint32_t ring = lds_addr(s_ring);
-  uint32_t a_rd[2], w_rd[2];                          // this lane's fragments of the two 32-k steps
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t ch = (uint32_t)(((2 * c + g) ^ swz(r32)) << 4);
-    a_rd[c] = (uint32_t)((half * 128 + r32) * kBK) + ch;
-    w_rd[c] = (uint32_t)(kBigA + (wn * 64 + r32) * kBK) + ch;
-  }
+  // this lane's 16 bytes of the first fragment of either operand
+  const uint32_t ch = (uint32_t)((g ^ swz(r16)) << 4);
+  const uint32_t a_rd = (uint32_t)((half * 128 + r16) * kBK) + ch;
+  const uint32_t w_rd = (uint32_t)(kBigA + (wn * 64 + r16) * kBK) + ch;
 
   // ---- the copy cursor: stage cur_s of tile cur_t is the next to be copied.  When
   // every stage is, the last is copied again into slots nobody reads, so that
@@ -281,31 +284,26 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
     }
   };
 
-  i32x16 acc[4][2];
-  i32x4 fa[4][2], fw[2][2];
+  i32x4 acc[8][4];
+  i32x4 fa[8], fw[4];
   auto read_stage = [&](int slot) QMOE_INLINE {
     const uint8_t *base = s_ring + slot * kBigSlot;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int j = 0; j < 4; ++j) fw[j] = *reinterpret_cast<const i32x4 *>(base + w_rd + j * 16 * kBK);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        fw[j][c] = *reinterpret_cast<const i32x4 *>(base + w_rd[c] + j * 32 * kBK);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        fa[i][c] = *reinterpret_cast<const i32x4 *>(base + a_rd[c] + i * 32 * kBK);
-    }
+    for (int i = 0; i < 8; ++i) fa[i] = *reinterpret_cast<const i32x4 *>(base + a_rd + i * 16 * kBK);
   };
-  // the products of a stage, with (kDma) the cursor's copies between them
+  // the products of a stage, with (with_dma) the cursor's copies between them
   auto multiply = [&](auto with_dma) QMOE_INLINE {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int c = q >> 3, j = (q >> 2) & 1, i = q & 3;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+    for (int q = 0; q < 32; ++q) {
+      const int j = q >> 3, i = q & 7;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
       if constexpr (decltype(with_dma)::value) {
-        if ((q & 3) == 1) {
+        if ((q & 7) == 3) {
           __builtin_amdgcn_sched_barrier(0);
-          dma_piece(q >> 2);
+          dma_piece(q >> 3);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -338,11 +336,9 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
       side = p.a_scale[min(m0 + tid - kBN, p.M - 1)];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+      for (int j = 0; j < 4; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
     // Phase 2 s: the upper half reads stage s; phase 2 s + 1: the lower half
     // does.  Stage s + 1 has to be there after phase 2 s + 1, when the upper half
@@ -405,15 +401,12 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
     wait_lds();
     phase_end();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ml = half * 128 + 32 * i + r32;
+    for (int i = 0; i < 8; ++i) {
+      const int ml = half * 128 + 16 * i + r16;
       const float sa = s_sa[ml];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          store_run<Ty>(p, m0 + ml, n0, wn * 64 + 32 * j + 16 * kk, g, sa, s_sw, s_bias, acc[i][j],
-                        8 * kk);
+      for (int j = 0; j < 4; j += 2)
+        store_run<Ty>(p, m0 + ml, n0, wn * 64 + 16 * j, g, sa, s_sw, s_bias, acc[i][j], acc[i][j + 1]);
     }
     t += gx;
     if (t >= t_end) break;
