@@ -1,8 +1,6 @@
 // Dense int8 product with a scale per token and per output channel:
 //   out[m, n] = round((sum_k a[m,k] w[n,k]) * a_scale[m] * w_scale[n] + bias[n] + addend[m, n])
 // The sums are exact: int8 products added in int32 on the int8 MFMA.
-#include <type_traits>
-
 #include "qmoe_device.h"
 #include "qmoe_layer.h"
 
@@ -176,10 +174,10 @@ __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int 
 // phase: while one half reads a stage's fragments from LDS, the other multiplies
 // the stage that it read in the phase before, so that one of the two wavefronts
 // of every SIMD has products to do at any time.  A barrier ends each phase.  The
-// DMA of the stage three ahead goes out between the products, one copy every
-// four of them: issued in one go, the copies of a stage hold up their wavefronts
-// (128-k stages in two slots, all copies at once: 1900 cycles in that phase, 540
-// in the others, 244 us for 4096 x 14336 x 4096).
+// DMA of the stage three ahead goes out right behind a stage's reads, where the
+// wavefront would wait anyway: its copies queue up for the CU's one address path,
+// and between products they held those up (770-810 cycles for 512 cycles of
+// products; all copies of a 128-k stage at once in two slots: 1900).
 constexpr int kBM = 256, kBN = 256, kBK = 64;
 constexpr int kBigThreads = 512;
 constexpr int kRing = 4;
@@ -293,32 +291,28 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
 #pragma unroll
     for (int i = 0; i < 8; ++i) fa[i] = *reinterpret_cast<const i32x4 *>(base + a_rd + i * 16 * kBK);
   };
-  // the products of a stage, with (with_dma) the cursor's copies between them
-  auto multiply = [&](auto with_dma) QMOE_INLINE {
+  auto multiply = [&]() QMOE_INLINE {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const int j = q >> 3, i = q & 7;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
-      if constexpr (decltype(with_dma)::value) {
-        if ((q & 7) == 3) {
-          __builtin_amdgcn_sched_barrier(0);
-          dma_piece(q >> 3);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
+  };
+  // the cursor's copies, behind a stage's reads
+  auto copy_stage = [&]() QMOE_INLINE {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kBigPieces; ++u) dma_piece(u);
+    dma_next();
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   if (full > 0) {
     enter(t);
 #pragma unroll
-    for (int d = 0; d < kRing - 1; ++d) {
-#pragma unroll
-      for (int u = 0; u < kBigPieces; ++u) dma_piece(u);
-      dma_next();
-    }
+    for (int d = 0; d < kRing - 1; ++d) copy_stage();
     wait_dma<2 * kBigPieces>();                       // stage 0 has landed here ...
   }
   phase_end();                                        // ... and everywhere
@@ -342,15 +336,15 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
 
     // Phase 2 s: the upper half reads stage s; phase 2 s + 1: the lower half
     // does.  Stage s + 1 has to be there after phase 2 s + 1, when the upper half
-    // has issued the copies up to stage s + 3, the lower half up to s + 2.
+    // as the lower has issued the copies up to stage s + 3.
     if (full > 0) {
       if (half == 0) {
         for (int s = 0; s < full; ++s) {
           read_stage(slot);
+          copy_stage();
           wait_lds();
           phase_end();
-          multiply(std::true_type{});
-          dma_next();
+          multiply();
           wait_dma<2 * kBigPieces>();
           phase_end();
           slot = (slot + 1) & (kRing - 1);
@@ -360,11 +354,11 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
         phase_end();
         for (int s = 0; s < full; ++s) {
           read_stage(slot);
+          copy_stage();
           wait_lds();
-          wait_dma<kBigPieces>();
+          wait_dma<2 * kBigPieces>();
           phase_end();
-          multiply(std::true_type{});
-          dma_next();
+          multiply();
           phase_end();
           slot = (slot + 1) & (kRing - 1);
         }
@@ -387,7 +381,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
       wait_lds();
       phase_end();
       read_stage(ts);
-      multiply(std::false_type{});
+      multiply();
       wait_lds();
       phase_end();
     }
