@@ -34,43 +34,47 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
   return v;
 }
 
-// 64 x 64 tile, four wavefronts of 32 x 32 (v_mfma_i32_32x32x32_i8, weights as
-// the first operand), 64 k a stage through LDS rows of 80 bytes.
-constexpr int kRow = 80;
+// Any row distance, address and K: 64 x 64 tiles, four wavefronts of 32 x 32
+// (v_mfma_i32_32x32x32_i8, weights as the first operand), 64 k a stage through
+// registers into LDS rows of 80 bytes.
+constexpr int kAnyRow = 80;
+constexpr long long kAnyGrid = 1 << 20;
 template <typename Ty>
 __global__ __launch_bounds__(256) void int8_any_kernel(const Int8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[64 * kRow], s_w[64 * kRow];
+  __shared__ __attribute__((aligned(16))) uint8_t s_a[64 * kAnyRow], s_w[64 * kAnyRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   const int r = tid >> 2, c = (tid & 3) * 16;        // this thread's row and chunk of a stage
-  const bool am = m0 + r < p.M, wn = n0 + r < p.N;
-  const int8_t *ar = p.a + (long long)(am ? m0 + r : 0) * p.lda;
-  const int8_t *wr = p.w + (long long)(wn ? n0 + r : 0) * p.ldw;
-  i32x16 acc;
-#pragma unroll
-  for (int v = 0; v < 16; ++v) acc[v] = 0;
   const int g = lane >> 5, q = lane & 31;
   const int mw = (wave & 1) * 32, nw = (wave >> 1) * 32;
-  for (int k = 0; k < p.K; k += 64) {
-    const i32x4 z = {0, 0, 0, 0};
-    const i32x4 av = am ? load16(ar, k + c, p.K) : z;
-    const i32x4 wv = wn ? load16(wr, k + c, p.K) : z;
-    __syncthreads();
-    *reinterpret_cast<i32x4 *>(s_a + r * kRow + c) = av;
-    *reinterpret_cast<i32x4 *>(s_w + r * kRow + c) = wv;
-    __syncthreads();
+  const long long ntn = (p.N + 63) / 64, tiles = (p.M + 63ll) / 64 * ntn;
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int m0 = (int)(t / ntn) * 64, n0 = (int)(t % ntn) * 64;
+    const bool am = r < p.M - m0, wn = r < p.N - n0;
+    const int8_t *ar = p.a + (long long)(am ? m0 + r : 0) * p.lda;
+    const int8_t *wr = p.w + (long long)(wn ? n0 + r : 0) * p.ldw;
+    i32x16 acc;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_a + (mw + q) * kRow + 32 * h + 16 * g);
-      const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_w + (nw + q) * kRow + 32 * h + 16 * g);
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, fa, acc, 0, 0, 0);
+    for (int v = 0; v < 16; ++v) acc[v] = 0;
+    for (int k = 0; k < p.K; k += 64) {
+      const i32x4 z = {0, 0, 0, 0};
+      const i32x4 av = am ? load16(ar, k + c, p.K) : z;
+      const i32x4 wv = wn ? load16(wr, k + c, p.K) : z;
+      __syncthreads();
+      *reinterpret_cast<i32x4 *>(s_a + r * kAnyRow + c) = av;
+      *reinterpret_cast<i32x4 *>(s_w + r * kAnyRow + c) = wv;
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_a + (mw + q) * kAnyRow + 32 * h + 16 * g);
+        const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_w + (nw + q) * kAnyRow + 32 * h + 16 * g);
+        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, fa, acc, 0, 0, 0);
+      }
     }
-  }
-  const int m = m0 + mw + q;
 #pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    const int n = n0 + nw + 8 * (v >> 2) + 4 * g + (v & 3);
-    if (m < p.M && n < p.N) store_one<Ty>(p, m, n, acc[v]);
+    for (int v = 0; v < 16; ++v) {
+      const int ml = mw + q, nl = nw + 8 * (v >> 2) + 4 * g + (v & 3);
+      if (ml < p.M - m0 && nl < p.N - n0) store_one<Ty>(p, m0 + ml, n0 + nl, acc[v]);
+    }
   }
 }
 
@@ -408,9 +412,503 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
   wait_dma_all();                                     // no copy into LDS outlives the workgroup
 }
 
-}  // namespace
+// ---- few rows: weights straight into registers ------------------------------------
+// One workgroup of kW wavefronts per 16 MB rows x 16 C columns.  The wavefronts
+// share out the contraction (128 k each in turn), load both operands' MFMA
+// fragments straight from memory (any alignment), two such steps ahead, and add
+// their exact partial sums through LDS at the end.  No barrier and no LDS until
+// then, so the loads of every wavefront are always under way: what a weight-bound
+// product needs.
+template <typename Ty>
+__device__ __forceinline__ void store_four(const Int8Args &p, int m, int n, float sa, const float *sw,
+                                           const float *bias, const i32x4 &sum) {
+  typedef typename Ty::T T;
+  if (m >= p.M) return;
+  const long long at = (long long)m * p.ldo + n;
+  const T *add = (const T *)p.addend + at;
+  T *out = (T *)p.out + at;
+  float f[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f[c] = (float)sum[c] * sa * sw[c];
+    if (p.bias) f[c] += bias[c];
+  }
+  if (n + 4 <= p.N) {
+    if constexpr (sizeof(T) == 4) {
+      if (p.addend) {
+        const f32x4u q = *reinterpret_cast<const f32x4u *>(add);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] += q[c];
+      }
+      *reinterpret_cast<f32x4u *>(out) = f32x4{f[0], f[1], f[2], f[3]};
+    } else {
+      if (p.addend) {
+        const i32x2u q = *reinterpret_cast<const i32x2u *>(add);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] += Ty::load((T)(q[c >> 1] >> (16 * (c & 1))));
+      }
+      *reinterpret_cast<i32x2u *>(out) = i32x2{Ty::pack(f[0], f[1]), Ty::pack(f[2], f[3])};
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < p.N) out[c] = Ty::store(p.addend ? f[c] + Ty::load(add[c]) : f[c]);
+  }
+}
 
-size_t int8_workspace_bytes(int, int, int) { return 0; }
+// 16 bytes of a row of at least 16 from byte k on, zero past K: the row's last 16
+// bytes moved down.
+__device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
+  const int at = min(k, K - 16), drop = 8 * (k - at);  // bits
+  uint64_t v[2];
+  __builtin_memcpy(v, row + at, 16);
+  const uint64_t lo = drop < 64 ? (v[0] >> drop) | (v[1] << 1 << (63 - drop)) : v[1] >> (drop & 63);
+  const uint64_t hi = drop < 64 ? v[1] >> drop : 0;
+  v[0] = k < K ? lo : 0;
+  v[1] = k < K ? hi : 0;
+  return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+}
+
+template <typename Ty, int MB, int C, int kW>
+__global__ __launch_bounds__(64 * kW) void int8_direct_kernel(const Int8Args p, int col_tiles) {
+  constexpr int kStep = 128;                          // k of a wavefront's step: whole lines
+  __shared__ __attribute__((aligned(16))) i32x4 s_part[kW][MB * C][64];
+  __shared__ float s_sa[16 * MB], s_sw[16 * C], s_bias[16 * C];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, r16 = lane & 15;
+  const int m0 = (blockIdx.x / col_tiles) * (16 * MB), n0 = (blockIdx.x % col_tiles) * (16 * C);
+  for (int i = tid; i < 16 * C; i += 64 * kW) {
+    s_sw[i] = p.w_scale[min(n0 + i, p.N - 1)];
+    if (p.bias) s_bias[i] = p.bias[min(n0 + i, p.N - 1)];
+  }
+  for (int i = tid; i < 16 * MB; i += 64 * kW) s_sa[i] = p.a_scale[min(m0 + i, p.M - 1)];
+
+  // rows past the last repeat it; their results are not stored
+  const int8_t *a0 = p.a + (long long)m0 * p.lda, *w0 = p.w + (long long)n0 * p.ldw;
+  uint32_t a_off[MB], w_off[C];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    a_off[i] = (uint32_t)min(16 * i + r16, p.M - 1 - m0) * (uint32_t)p.lda + 16u * g;
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    w_off[j] = (uint32_t)min(16 * j + r16, p.N - 1 - n0) * (uint32_t)p.ldw + 16u * g;
+
+  i32x4 acc[MB][C];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  struct Step {
+    i32x4 a[MB][2], w[C][2];
+  };
+  auto load = [&](Step &f, int k0) QMOE_INLINE {
+    if (k0 + kStep <= p.K) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) __builtin_memcpy(&f.w[j][c], w0 + k0 + 64 * c + w_off[j], 16);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) __builtin_memcpy(&f.a[i][c], a0 + k0 + 64 * c + a_off[i], 16);
+      }
+    } else if (k0 < p.K) {                            // the last bytes of the rows
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = k0 + 64 * c + 16 * g;
+#pragma unroll
+        for (int j = 0; j < C; ++j) f.w[j][c] = load_end(w0 + w_off[j] - 16 * g, k, p.K);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) f.a[i][c] = load_end(a0 + a_off[i] - 16 * g, k, p.K);
+      }
+    }
+  };
+  auto multiply = [&](const Step &f) QMOE_INLINE {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[j][c], f.a[i][c], acc[i][j], 0, 0, 0);
+  };
+  // this wavefront's steps wave, wave + kW, ..; every workgroup begins at another
+  const int n = ((p.K + kStep - 1) / kStep - wave + kW - 1) / kW;
+  Step f0, f1;
+  int at = n > 0 ? (int)(blockIdx.x / kXcds) % n : 0;
+  auto next = [&]() QMOE_INLINE -> int {
+    const int k = (at * kW + wave) * kStep;
+    at = at + 1 < n ? at + 1 : 0;
+    return k;
+  };
+  if (n > 0) load(f0, next());
+  if (n > 1) load(f1, next());
+  for (int i = 0; i < n; i += 2) {
+    multiply(f0);
+    if (i + 2 < n) load(f0, next());
+    if (i + 1 >= n) break;
+    multiply(f1);
+    if (i + 3 < n) load(f1, next());
+  }
+
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) s_part[wave][i * C + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int f = wave; f < MB * C; f += kW) {
+    i32x4 sum = s_part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) sum += s_part[w][f][lane];
+    const int i = f / C, col = 16 * (f - i * C) + 4 * g;
+    store_four<Ty>(p, m0 + 16 * i + r16, n0 + col, s_sa[16 * i + r16], s_sw + col, s_bias + col, sum);
+  }
+}
+
+// ---- few rows, aligned: weights through each wavefront's own LDS ----------------------
+// As int8_direct_kernel, but a step's rows come as whole 128-byte lines by
+// direct-to-LDS DMA into the wavefront's own ring of kD steps, from where the
+// fragments are read.  (A fragment's 64 lanes read 16 rows, neighbouring lanes in
+// different rows: straight from memory that is 64 line look-ups for 1 KB, and the
+// cache's look-ups bound the kernel.)  A wavefront waits only for its own copies.
+// AI: copies of activation rows a step, 8 rows each.
+// With `splits` > 1, workgroup (tile, y) contracts the y-th share of k and leaves
+// its sums in p.ws for int8_join_kernel.
+__device__ __forceinline__ int padded_cols(int N) { return (N + 3) & ~3; }
+
+template <typename Ty, int MB, int C, int kW, int kD, int AI>
+__global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, int col_tiles,
+                                                              int splits) {
+  constexpr int kStep = 128, kRows = 16 * (MB + C), kSlot = kRows * kStep;
+  constexpr int kPieces = AI + 2 * C;
+  constexpr int kRingBytes = kW * kD * kSlot, kPartBytes = kW * MB * C * 1024;
+  static_assert((kD - 1) * kPieces < 64, "the copies in flight are counted in 6 bits");
+  __shared__ __attribute__((aligned(1024))) uint8_t
+      s_ring[kRingBytes > kPartBytes ? kRingBytes : kPartBytes];   // the partial sums reuse it
+  __shared__ float s_sa[16 * MB], s_sw[16 * C], s_bias[16 * C];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, r16 = lane & 15;
+  const int m0 = (blockIdx.x / col_tiles) * (16 * MB), n0 = (blockIdx.x % col_tiles) * (16 * C);
+  const int8_t *a0 = p.a + (long long)m0 * p.lda, *w0 = p.w + (long long)n0 * p.ldw;
+
+  // 16-byte chunk c of LDS row r lies at c ^ ((r >> 1) & 7)
+  uint32_t a_off[AI], w_off[2 * C];
+#pragma unroll
+  for (int u = 0; u < AI; ++u) {
+    const int r = 8 * u + (lane >> 3);
+    a_off[u] = (uint32_t)min(r, p.M - 1 - m0) * (uint32_t)p.lda +
+               16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+  }
+#pragma unroll
+  for (int u = 0; u < 2 * C; ++u) {
+    const int r = 8 * u + (lane >> 3);
+    w_off[u] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.ldw +
+               16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+  }
+  uint8_t *mine = s_ring + wave * kD * kSlot;
+  const uint32_t ring = lds_addr(mine);
+  auto copy = [&](int slot, int k0) QMOE_INLINE {
+    const uint32_t at = ring + (uint32_t)(slot * kSlot);
+#pragma unroll
+    for (int u = 0; u < 2 * C; ++u) dma16(w0 + k0, w_off[u], at + (uint32_t)(16 * MB * kStep + u * 1024));
+#pragma unroll
+    for (int u = 0; u < AI; ++u) dma16(a0 + k0, a_off[u], at + (uint32_t)(u * 1024));
+  };
+
+  i32x4 acc[MB][C];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  // this wavefront's whole steps turn, turn + turns, ..; every workgroup begins at
+  // another (a few percent where they all run through the same lines of k)
+  const int turn = (int)blockIdx.y * kW + wave, turns = splits * kW;
+  const int whole = p.K / kStep, n = (whole - turn + turns - 1) / turns;
+  int at = n > 0 ? (int)(blockIdx.x / kXcds) % n : 0;
+  auto next = [&]() QMOE_INLINE -> int {
+    const int k = (at * turns + turn) * kStep;
+    at = at + 1 < n ? at + 1 : 0;
+    return k;
+  };
+#pragma unroll
+  for (int d = 0; d < kD; ++d)
+    if (d < n) copy(d, next());
+  // scales and bias, behind the first copies
+  float side = 0.0f, side2 = 0.0f;
+  const int q = tid - 16 * C;
+  if (tid < 16 * C) {
+    side = p.w_scale[min(n0 + tid, p.N - 1)];
+    if (p.bias) side2 = p.bias[min(n0 + tid, p.N - 1)];
+  } else if (q < 16 * MB) {
+    side = p.a_scale[min(m0 + q, p.M - 1)];
+  }
+  static_assert(16 * (MB + C) <= 64 * kW, "a thread for every scale");
+  const uint32_t sw = (uint32_t)((r16 >> 1) & 7);
+  int slot = 0;
+  for (int i = 0; i < n; ++i) {
+    if (i + kD <= n) wait_dma<(kD - 1) * kPieces>();
+    else wait_dma_all();
+    const uint8_t *base = mine + slot * kSlot + r16 * kStep;
+    i32x4 fa[MB][2], fw[C][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t ch = (((uint32_t)(4 * c + g)) ^ sw) << 4;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        fw[j][c] = *reinterpret_cast<const i32x4 *>(base + ch + 16 * (MB + j) * kStep);
+#pragma unroll
+      for (int ii = 0; ii < MB; ++ii)
+        fa[ii][c] = *reinterpret_cast<const i32x4 *>(base + ch + 16 * ii * kStep);
+    }
+    wait_lds();                                       // the slot has been read
+    if (i + kD < n) copy(slot, next());
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int ii = 0; ii < MB; ++ii)
+          acc[ii][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j][c], fa[ii][c], acc[ii][j], 0, 0, 0);
+    slot = slot + 1 < kD ? slot + 1 : 0;
+  }
+  // the last bytes of the rows, by the wavefront whose turn it is
+  if (p.K > whole * kStep && whole % turns == turn) {
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      const int k = whole * kStep + 64 * c + 16 * g;
+      i32x4 fa[MB], fw[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        fw[j] = load16(w0 + (long long)min(16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        fa[i] = load16(a0 + (long long)min(16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+
+  if (tid < 16 * C) {
+    s_sw[tid] = side;
+    s_bias[tid] = side2;
+  } else if (q < 16 * MB) {
+    s_sa[q] = side;
+  }
+  __syncthreads();                                    // every wavefront is done with its ring
+  i32x4 *part = reinterpret_cast<i32x4 *>(s_ring);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) part[(wave * MB * C + i * C + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int f = wave; f < MB * C; f += kW) {
+    i32x4 sum = part[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) sum += part[(w * MB * C + f) * 64 + lane];
+    const int i = f / C, col = 16 * (f - i * C) + 4 * g, m = m0 + 16 * i + r16, nn = n0 + col;
+    if (splits == 1) {
+      store_four<Ty>(p, m, nn, s_sa[16 * i + r16], s_sw + col, s_bias + col, sum);
+    } else if (m < p.M && nn < p.N) {
+      const long long np = padded_cols(p.N);
+      *reinterpret_cast<i32x4 *>(p.ws + ((long long)blockIdx.y * p.M + m) * np + nn) = sum;
+    }
+  }
+}
+
+// The shares' exact sums added, four columns a thread, and the epilogue.
+template <typename Ty>
+__global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args p, int splits) {
+  const int np = padded_cols(p.N), quads = np / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)p.M * quads) return;
+  const int m = (int)(i / quads), n = (int)(i - (long long)m * quads) * 4;
+  i32x4 sum = {0, 0, 0, 0};
+  for (int y = 0; y < splits; ++y)
+    sum += *reinterpret_cast<const i32x4 *>(p.ws + ((long long)y * p.M + m) * np + n);
+  float sw[4], bias[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    sw[c] = p.w_scale[min(n + c, p.N - 1)];
+    bias[c] = p.bias ? p.bias[min(n + c, p.N - 1)] : 0.0f;
+  }
+  store_four<Ty>(p, m, n, p.a_scale[m], sw, bias, sum);
+}
+
+// ---- a few hundred rows: 128 x 128 tiles, the contraction in two halves -----------------
+// Eight wavefronts in two groups of four; each group contracts one half of k over
+// the whole tile (wavefront: 64 x 64 outputs), with its own ring of four 64-k
+// stages, so every SIMD has two wavefronts even where the output has no more
+// tiles than the card CUs.  A stage's fragments are read while the one before is
+// multiplied; one barrier a stage.  The groups' exact sums meet in LDS.
+constexpr int kMM = 128, kMN = 128;
+constexpr int kMidSlot = (kMM + kMN) * kBK;          // 16 KB
+constexpr int kMidPieces = 4;
+
+template <typename Ty>
+__global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, TileOrder order) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kRing * kMidSlot];
+  __shared__ float s_sa[kMM], s_sw[kMN], s_bias[kMN];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave >> 2, wm = wave & 1, wn = (wave >> 1) & 1;
+  const int g = lane >> 4, r16 = lane & 15;
+  const int total = order.ntm * order.ntn, run = (total + kXcds - 1) / kXcds;
+  const int t = (int)(blockIdx.x & (kXcds - 1)) * run + (int)blockIdx.x / kXcds;
+  if ((int)blockIdx.x / kXcds >= run || t >= total) return;
+  int tm, tn;
+  order.at(t, tm, tn);
+  const int m0 = tm * kMM, n0 = tn * kMN;
+  const int8_t *a0 = p.a + (long long)m0 * p.lda, *w0 = p.w + (long long)n0 * p.ldw;
+
+  const int whole = p.K / kBK;                        // whole stages: group 0 the first half
+  const int first = grp ? (whole + 1) / 2 : 0;
+  const int mine = grp ? whole / 2 : (whole + 1) / 2, steps = (whole + 1) / 2;
+
+  // this wavefront's copies: rows 32 w .. of both operands, w its number in the group
+  const int w4 = wave & 3;
+  uint32_t a_off[2], w_off[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = 32 * w4 + 16 * u + (lane >> 2);
+    const uint32_t ch = 16u * (uint32_t)((lane & 3) ^ swz(r));
+    a_off[u] = (uint32_t)min(r, p.M - 1 - m0) * (uint32_t)p.lda + ch;
+    w_off[u] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.ldw + ch;
+  }
+  uint8_t *base = s_ring + grp * kRing * kMidSlot;
+  const uint32_t ring = lds_addr(base);
+  // past the last stage it is copied again, into a slot that is not read any more
+  auto copy = [&](int s) QMOE_INLINE {
+    const int k0 = (first + min(s, mine - 1)) * kBK;
+    const uint32_t at = ring + (uint32_t)((s & (kRing - 1)) * kMidSlot + w4 * 2048);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) dma16(a0 + k0, a_off[u], at + (uint32_t)(u * 1024));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) dma16(w0 + k0, w_off[u], at + (uint32_t)(kMM * kBK + u * 1024));
+  };
+  const uint32_t ch = (uint32_t)((g ^ swz(r16)) << 4);
+  const uint32_t a_rd = (uint32_t)((wm * 64 + r16) * kBK) + ch;
+  const uint32_t w_rd = (uint32_t)((kMM + wn * 64 + r16) * kBK) + ch;
+  struct Frags {
+    i32x4 a[4], w[4];
+  };
+  auto read = [&](Frags &f, int s) QMOE_INLINE {
+    const uint8_t *q = base + (s & (kRing - 1)) * kMidSlot;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.w[j] = *reinterpret_cast<const i32x4 *>(q + w_rd + j * 16 * kBK);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.a[i] = *reinterpret_cast<const i32x4 *>(q + a_rd + i * 16 * kBK);
+  };
+  i32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](const Frags &f) QMOE_INLINE {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[j], f.a[i], acc[i][j], 0, 0, 0);
+  };
+
+  float side = 0.0f, side2 = 0.0f;
+  Frags f0, f1;
+  if (mine > 0) {
+#pragma unroll
+    for (int s = 0; s < kRing; ++s) copy(s);
+  }
+  if (tid < kMN) {
+    side = p.w_scale[min(n0 + tid, p.N - 1)];
+    if (p.bias) side2 = p.bias[min(n0 + tid, p.N - 1)];
+  } else if (tid < kMN + kMM) {
+    side = p.a_scale[min(m0 + tid - kMN, p.M - 1)];
+  }
+  if (tid < kMN) {
+    s_sw[tid] = side;
+    s_bias[tid] = side2;
+  } else if (tid < kMN + kMM) {
+    s_sa[tid - kMN] = side;
+  }
+  // Stage s + 1 has landed everywhere, and everybody has read stage s, after the
+  // barrier of step s; the copies of the two stages behind it may be under way.
+  wait_dma<3 * kMidPieces>();
+  phase_end();
+  if (mine > 0) read(f0, 0);
+  wait_lds();
+  // a step's reads and copies go between its products, where they do not hold them up
+  auto step = [&](Frags &now, Frags &then, int s) QMOE_INLINE {
+    wait_dma<2 * kMidPieces>();
+    phase_end();
+    const uint8_t *q = base + ((s + 1) & (kRing - 1)) * kMidSlot;
+    const int k0 = (first + min(s + kRing, mine - 1)) * kBK;
+    const uint32_t at = ring + (uint32_t)((s & (kRing - 1)) * kMidSlot + w4 * 2048);
+    if (s < mine) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = e >> 2, i = e & 3;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(now.w[j], now.a[i], acc[i][j], 0, 0, 0);
+        if ((e & 1) == 0) {
+          const int r = e >> 1;
+          if (r < 4) then.w[r] = *reinterpret_cast<const i32x4 *>(q + w_rd + r * 16 * kBK);
+          else then.a[r - 4] = *reinterpret_cast<const i32x4 *>(q + a_rd + (r - 4) * 16 * kBK);
+        } else if ((e & 3) == 3) {
+          const int u = e >> 2;
+          if (u < 2) dma16(a0 + k0, a_off[u], at + (uint32_t)(u * 1024));
+          else dma16(w0 + k0, w_off[u - 2], at + (uint32_t)(kMM * kBK + (u - 2) * 1024));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_lds();
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(f0, f1, s);
+    if (s + 1 < steps) step(f1, f0, s + 1);
+  }
+  // the last bytes of the rows, straight from memory
+  if (grp == 1 && p.K > whole * kBK) {
+    const int k = whole * kBK + 16 * g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f0.w[j] = load_end(w0 + (long long)min(wn * 64 + 16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f0.a[i] = load_end(a0 + (long long)min(wm * 64 + 16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
+    multiply(f0);
+  }
+
+  wait_dma_all();                                     // no copy lands in what follows
+  phase_end();
+  // group 0 finishes the rows i = 0, 1 of its wavefronts, group 1 the rows i = 2, 3
+  i32x4 *part = reinterpret_cast<i32x4 *>(s_ring);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      part[((wave * 2 + i) * 4 + j) * 64 + lane] = grp ? acc[i][j] : acc[i + 2][j];
+  wait_lds();
+  phase_end();
+  const int other = wave ^ 4;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int ml = wm * 64 + 16 * (2 * grp + i) + r16;
+    const float sa = s_sa[ml];
+    i32x4 sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sum[j] = (grp ? acc[i + 2][j] : acc[i][j]) + part[((other * 2 + i) * 4 + j) * 64 + lane];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+      store_run<Ty>(p, m0 + ml, n0, wn * 64 + 16 * j, g, sa, s_sw, s_bias, sum[j], sum[j + 1]);
+  }
+}
+
+}  // namespace
 
 namespace {
 
@@ -422,25 +920,128 @@ int compute_units() {
   return n;
 }
 
+long long tiles_of(int M, int N, int tm, int tn) {
+  return (long long)((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+}
+
+// The kernels and their tiles.  Time goes by rounds of one workgroup a CU; at
+// K = 4096 a round of 64 x 64 tiles (int8_staged_kernel) takes 7.2 us, of 128 x
+// 128 tiles (int8_mid_kernel) 21 us, of 256 x 256 tiles (int8_big_kernel) 40 us,
+// and all grow with K alike, so the fewest microseconds by that count win.
+// Measured on both sides of the borders (us, staged / mid / big): 512 x 4096 x
+// 4096 19 / 21 / 38, 1024 x 4096 x 4096 36 / 25 / 39, 2048 x 4096 x 4096 69 / 47
+// / 40, 512 x 4096 x 14336 73 / 45 / 40 (M x K x N).
+enum Kind { kStaged, kMid, kBig };
+constexpr int kCus = 256;
+Kind kind_of(int M, int N) {
+  auto rounds = [&](int tm, int tn) { return (tiles_of(M, N, tm, tn) + kCus - 1) / kCus; };
+  const double staged = 7.2 * rounds(64, 64), mid = 21.0 * rounds(kMM, kMN),
+               big = 40.0 * rounds(kBM, kBN);
+  if (M <= 64 || (staged <= mid && staged <= big)) return kStaged;
+  return mid < big ? kMid : kBig;
+}
+
+// Tiles of int8_staged_kernel: 16 rows for up to 16, 32 for up to 32, else 64; the
+// widest columns that still give most CUs a workgroup (64 x 4096 x 4096: 16
+// columns 6.4 us, 32 7.3, 64 9.7; 64 x 4096 x 14336: 20.5, 14.5, 12.9).
+struct StagedShape {
+  int mb, c, splits;
+};
+StagedShape staged_shape(int M, int K, int N) {
+  StagedShape t{M <= 16 ? 1 : M <= 32 ? 2 : 4, 1, 1};
+  const int widest = t.mb == 1 ? 2 : 4;
+  while (t.c < widest && tiles_of(M, N, 16 * t.mb, 32 * t.c) >= 192) t.c *= 2;
+  // Shares of k where the tiles leave three quarters of the CUs idle and each
+  // has a long way to go: 512 k of every wavefront (a second launch costs 4 us)
+  const long long tiles = tiles_of(M, N, 16 * t.mb, 16 * t.c);
+  if (tiles <= kCus / 4) {
+    const long long room = kCus / tiles, work = K / 2048;
+    t.splits = (int)(room < work ? room : work);
+    if (t.splits < 3) t.splits = 1;
+  }
+  return t;
+}
+
+size_t staged_bytes(const StagedShape &t, int M, int N) {
+  return t.splits == 1 ? 0 : (size_t)t.splits * M * ((N + 3) / 4 * 4) * sizeof(int);
+}
+
+template <typename Ty, int MB, int C, int kW, int kD, int AI>
+hipError_t launch_staged(const Int8Args &a, int splits, hipStream_t s) {
+  const int cols = (a.N + 16 * C - 1) / (16 * C), rows = (a.M + 16 * MB - 1) / (16 * MB);
+  hipLaunchKernelGGL((int8_staged_kernel<Ty, MB, C, kW, kD, AI>),
+                     dim3((unsigned)(cols * rows), (unsigned)splits), dim3(64 * kW), 0, s, a, cols,
+                     splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const long long quads = (long long)a.M * ((a.N + 3) / 4);
+  hipLaunchKernelGGL(int8_join_kernel<Ty>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a,
+                     splits);
+  return hipGetLastError();
+}
+
+template <typename Ty, int MB, int C, int kW>
+hipError_t launch_direct(const Int8Args &a, hipStream_t s) {
+  const int cols = (a.N + 16 * C - 1) / (16 * C), rows = (a.M + 16 * MB - 1) / (16 * MB);
+  hipLaunchKernelGGL((int8_direct_kernel<Ty, MB, C, kW>), dim3((unsigned)(cols * rows)), dim3(64 * kW),
+                     0, s, a, cols);
+  return hipGetLastError();
+}
+
 template <typename Ty>
 hipError_t launch(const Int8Args &a, hipStream_t s) {
   // rows that direct-to-LDS copies can take
   const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
                        a.ldw % 16 == 0;
-  if (aligned && a.M > 256) {
-    const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};
-    const long long tiles = (long long)order.ntm * order.ntn;
-    const int cus = compute_units();
-    hipLaunchKernelGGL(int8_big_kernel<Ty>, dim3((unsigned)(tiles < cus ? tiles : cus)),
-                       dim3(kBigThreads), 0, s, a, order);
+  if (!aligned) {
+    // rows at any byte: the loads straight into registers up to 256 rows, above
+    // that tiles shared in LDS (777 x 1536 x 4099: 34 us both)
+    if (a.K >= 16 && a.M <= 16) return launch_direct<Ty, 1, 1, 8>(a, s);
+    if (a.K >= 16 && a.M <= 256) return launch_direct<Ty, 4, 2, 4>(a, s);
+    const long long tiles = tiles_of(a.M, a.N, 64, 64);
+    hipLaunchKernelGGL(int8_any_kernel<Ty>, dim3((unsigned)(tiles < kAnyGrid ? tiles : kAnyGrid)),
+                       dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const dim3 g((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64)), b(256);
-  hipLaunchKernelGGL(int8_any_kernel<Ty>, g, b, 0, s, a);
+  const Kind kind = kind_of(a.M, a.N);
+  if (kind == kStaged) {
+    StagedShape t = staged_shape(a.M, a.K, a.N);
+    if (!a.ws) t.splits = 1;
+    if (t.mb == 1 && t.c == 1)
+      return a.M <= 8 ? launch_staged<Ty, 1, 1, 4, 4, 1>(a, t.splits, s)
+                      : launch_staged<Ty, 1, 1, 4, 4, 2>(a, t.splits, s);
+    if (t.mb == 1)
+      return a.M <= 8 ? launch_staged<Ty, 1, 2, 4, 3, 1>(a, t.splits, s)
+                      : launch_staged<Ty, 1, 2, 4, 3, 2>(a, t.splits, s);
+    if (t.mb == 2)
+      return t.c == 1   ? launch_staged<Ty, 2, 1, 4, 4, 4>(a, t.splits, s)
+             : t.c == 2 ? launch_staged<Ty, 2, 2, 4, 4, 4>(a, t.splits, s)
+                        : launch_staged<Ty, 2, 4, 4, 3, 4>(a, t.splits, s);
+    return t.c == 1   ? launch_staged<Ty, 4, 1, 4, 2, 8>(a, t.splits, s)
+           : t.c == 2 ? launch_staged<Ty, 4, 2, 4, 2, 8>(a, t.splits, s)
+                      : launch_staged<Ty, 4, 4, 4, 2, 8>(a, t.splits, s);
+  }
+  if (kind == kMid && a.K >= 16) {
+    const TileOrder order{(a.M + kMM - 1) / kMM, (a.N + kMN - 1) / kMN};
+    const long long tiles = (long long)order.ntm * order.ntn;
+    hipLaunchKernelGGL(int8_mid_kernel<Ty>, dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)),
+                       dim3(512), 0, s, a, order);
+    return hipGetLastError();
+  }
+  const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};
+  const long long tiles = (long long)order.ntm * order.ntn;
+  const int cus = compute_units();
+  hipLaunchKernelGGL(int8_big_kernel<Ty>, dim3((unsigned)(tiles < cus ? tiles : cus)),
+                     dim3(kBigThreads), 0, s, a, order);
   return hipGetLastError();
 }
 
 }  // namespace
+
+size_t int8_workspace_bytes(int M, int K, int N) {
+  if (kind_of(M, N) != kStaged) return 0;
+  return staged_bytes(staged_shape(M, K, N), M, N);
+}
 
 hipError_t launch_int8_gemm(const Int8Args &a, int out_dtype, hipStream_t s) {
   if (out_dtype == MOE_F32) return launch<TypeF32>(a, s);
