@@ -34,6 +34,19 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
   return v;
 }
 
+// 16 bytes of a row of at least 16 from byte k on, zero past K: the row's last 16
+// bytes moved down.
+__device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
+  const int at = min(k, K - 16), drop = 8 * (k - at);  // bits
+  uint64_t v[2];
+  __builtin_memcpy(v, row + at, 16);
+  const uint64_t lo = drop < 64 ? (v[0] >> drop) | (v[1] << 1 << (63 - drop)) : v[1] >> (drop & 63);
+  const uint64_t hi = drop < 64 ? v[1] >> drop : 0;
+  v[0] = k < K ? lo : 0;
+  v[1] = k < K ? hi : 0;
+  return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+}
+
 // Any row distance, address and K: 64 x 64 tiles, four wavefronts of 32 x 32
 // (v_mfma_i32_32x32x32_i8, weights as the first operand), 64 k a stage through
 // registers into LDS rows of 80 bytes.
@@ -380,7 +393,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
         const int8_t *row = is_a ? ar + (long long)min(r, p.M - 1 - m0) * p.lda
                                  : wr + (long long)min(r, p.N - 1 - n0) * p.ldw;
         *reinterpret_cast<i32x4 *>(s_ring + ts * kBigSlot + (is_a ? 0 : kBigA) + r * kBK +
-                                   ((c ^ swz(r)) << 4)) = load16(row, k0 + 16 * c, p.K);
+                                   ((c ^ swz(r)) << 4)) = load_end(row, k0 + 16 * c, p.K);
       }
       wait_lds();
       phase_end();
@@ -454,19 +467,6 @@ __device__ __forceinline__ void store_four(const Int8Args &p, int m, int n, floa
     for (int c = 0; c < 4; ++c)
       if (n + c < p.N) out[c] = Ty::store(p.addend ? f[c] + Ty::load(add[c]) : f[c]);
   }
-}
-
-// 16 bytes of a row of at least 16 from byte k on, zero past K: the row's last 16
-// bytes moved down.
-__device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
-  const int at = min(k, K - 16), drop = 8 * (k - at);  // bits
-  uint64_t v[2];
-  __builtin_memcpy(v, row + at, 16);
-  const uint64_t lo = drop < 64 ? (v[0] >> drop) | (v[1] << 1 << (63 - drop)) : v[1] >> (drop & 63);
-  const uint64_t hi = drop < 64 ? v[1] >> drop : 0;
-  v[0] = k < K ? lo : 0;
-  v[1] = k < K ? hi : 0;
-  return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
 }
 
 template <typename Ty, int MB, int C, int kW>
@@ -585,6 +585,7 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
   static_assert((kD - 1) * kPieces < 64, "the copies in flight are counted in 6 bits");
   __shared__ __attribute__((aligned(1024))) uint8_t
       s_ring[kRingBytes > kPartBytes ? kRingBytes : kPartBytes];   // the partial sums reuse it
+  __shared__ __attribute__((aligned(1024))) uint8_t s_end[kSlot];    // a last, shorter step
   __shared__ float s_sa[16 * MB], s_sw[16 * C], s_bias[16 * C];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -632,6 +633,25 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
     at = at + 1 < n ? at + 1 : 0;
     return k;
   };
+  // The 16-byte chunks behind the whole steps are a step of the wavefront whose
+  // turn it is, copied first (chunks past the last repeat it: activations are
+  // masked below).
+  const int end = whole * kStep, chunks = (p.K - end) / 16, rest = (p.K - end) & 15;
+  const bool ends = whole % turns == turn;
+  if (ends && chunks > 0) {
+    const uint32_t at_end = lds_addr(s_end);
+#pragma unroll
+    for (int u = 0; u < 2 * C; ++u) {
+      const int r = 8 * u + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      dma16(w0 + end, w_off[u] - 16u * (uint32_t)max(0, c - (chunks - 1)),
+            at_end + (uint32_t)(16 * MB * kStep + u * 1024));
+    }
+#pragma unroll
+    for (int u = 0; u < AI; ++u) {
+      const int r = 8 * u + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      dma16(a0 + end, a_off[u] - 16u * (uint32_t)max(0, c - (chunks - 1)), at_end + (uint32_t)(u * 1024));
+    }
+  }
 #pragma unroll
   for (int d = 0; d < kD; ++d)
     if (d < n) copy(d, next());
@@ -646,12 +666,9 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
   }
   static_assert(16 * (MB + C) <= 64 * kW, "a thread for every scale");
   const uint32_t sw = (uint32_t)((r16 >> 1) & 7);
-  int slot = 0;
-  for (int i = 0; i < n; ++i) {
-    if (i + kD <= n) wait_dma<(kD - 1) * kPieces>();
-    else wait_dma_all();
-    const uint8_t *base = mine + slot * kSlot + r16 * kStep;
-    i32x4 fa[MB][2], fw[C][2];
+  i32x4 fa[MB][2], fw[C][2];
+  auto read = [&](const uint8_t *from) QMOE_INLINE {
+    const uint8_t *base = from + r16 * kStep;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint32_t ch = (((uint32_t)(4 * c + g)) ^ sw) << 4;
@@ -659,38 +676,50 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
       for (int j = 0; j < C; ++j)
         fw[j][c] = *reinterpret_cast<const i32x4 *>(base + ch + 16 * (MB + j) * kStep);
 #pragma unroll
-      for (int ii = 0; ii < MB; ++ii)
-        fa[ii][c] = *reinterpret_cast<const i32x4 *>(base + ch + 16 * ii * kStep);
+      for (int i = 0; i < MB; ++i)
+        fa[i][c] = *reinterpret_cast<const i32x4 *>(base + ch + 16 * i * kStep);
     }
-    wait_lds();                                       // the slot has been read
-    if (i + kD < n) copy(slot, next());
+  };
+  auto multiply = [&](int c) QMOE_INLINE {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int ii = 0; ii < MB; ++ii)
-          acc[ii][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j][c], fa[ii][c], acc[ii][j], 0, 0, 0);
-    slot = slot + 1 < kD ? slot + 1 : 0;
-  }
-  // the last bytes of the rows, by the wavefront whose turn it is
-  if (p.K > whole * kStep && whole % turns == turn) {
-#pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      const int k = whole * kStep + 64 * c + 16 * g;
-      i32x4 fa[MB], fw[C];
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-        fw[j] = load16(w0 + (long long)min(16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+    for (int j = 0; j < C; ++j)
 #pragma unroll
       for (int i = 0; i < MB; ++i)
-        fa[i] = load16(a0 + (long long)min(16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+  };
+  int slot = 0;
+  for (int i = 0; i < n; ++i) {
+    if (i + kD <= n) wait_dma<(kD - 1) * kPieces>();
+    else wait_dma_all();
+    read(mine + slot * kSlot);
+    wait_lds();                                       // the slot has been read
+    if (i + kD < n) copy(slot, next());
+    multiply(0);
+    multiply(1);
+    slot = slot + 1 < kD ? slot + 1 : 0;
+  }
+  if (ends && chunks > 0) {
+    wait_dma_all();
+    read(s_end);
 #pragma unroll
-      for (int j = 0; j < C; ++j)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < MB; ++i)
+        if (4 * c + g >= chunks) fa[i][c] = i32x4{0, 0, 0, 0};
+      multiply(c);
     }
+  }
+  if (ends && rest > 0) {                             // the last bytes, straight from memory
+    const int k = p.K - rest;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      fw[j][0] = load_end(w0 + (long long)min(16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      fa[i][0] = load_end(a0 + (long long)min(16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
+      if (g > 0) fa[i][0] = i32x4{0, 0, 0, 0};
+    }
+    multiply(0);
   }
 
   if (tid < 16 * C) {
@@ -924,42 +953,50 @@ long long tiles_of(int M, int N, int tm, int tn) {
   return (long long)((M + tm - 1) / tm) * ((N + tn - 1) / tn);
 }
 
-// The kernels and their tiles.  Time goes by rounds of one workgroup a CU; at
-// K = 4096 a round of 64 x 64 tiles (int8_staged_kernel) takes 7.2 us, of 128 x
-// 128 tiles (int8_mid_kernel) 21 us, of 256 x 256 tiles (int8_big_kernel) 40 us,
-// and all grow with K alike, so the fewest microseconds by that count win.
-// Measured on both sides of the borders (us, staged / mid / big): 512 x 4096 x
+// The kernels and their tiles, by the time they take: rounds of one workgroup a CU
+// (two for the smallest), each as long as measured at K = 4096; all grow with K
+// alike, so the least time by that count wins.
+//
+// int8_staged_kernel, 16, 32 or 64 columns: a round of 4, 5, 7.5 us (64 x 4096 x
+// 4096: 6.4, 7.3, 9.7 us with the launch; 64 x 4096 x 14336: 20.5, 14.5, 12.9).
+// With up to 16 rows two workgroups fit a CU, 1 or 1.8 us a round of those (1 x
+// 4096 x 14336: 11.0 us with 16 columns, 10.3 with 32).
+// 128 x 128 tiles (int8_mid_kernel): 21 us; 256 x 256 (int8_big_kernel): 40 us.
+// On both sides of the borders (us, staged / mid / big, M x K x N): 512 x 4096 x
 // 4096 19 / 21 / 38, 1024 x 4096 x 4096 36 / 25 / 39, 2048 x 4096 x 4096 69 / 47
-// / 40, 512 x 4096 x 14336 73 / 45 / 40 (M x K x N).
-enum Kind { kStaged, kMid, kBig };
+// / 40, 512 x 4096 x 14336 73 / 45 / 40.
 constexpr int kCus = 256;
-Kind kind_of(int M, int N) {
-  auto rounds = [&](int tm, int tn) { return (tiles_of(M, N, tm, tn) + kCus - 1) / kCus; };
-  const double staged = 7.2 * rounds(64, 64), mid = 21.0 * rounds(kMM, kMN),
-               big = 40.0 * rounds(kBM, kBN);
-  if (M <= 64 || (staged <= mid && staged <= big)) return kStaged;
-  return mid < big ? kMid : kBig;
-}
-
-// Tiles of int8_staged_kernel: 16 rows for up to 16, 32 for up to 32, else 64; the
-// widest columns that still give most CUs a workgroup (64 x 4096 x 4096: 16
-// columns 6.4 us, 32 7.3, 64 9.7; 64 x 4096 x 14336: 20.5, 14.5, 12.9).
 struct StagedShape {
-  int mb, c, splits;
+  int mb, c, splits;                                  // 16 mb rows, 16 c columns, shares of k
+  double us;                                          // at K = 4096
 };
 StagedShape staged_shape(int M, int K, int N) {
-  StagedShape t{M <= 16 ? 1 : M <= 32 ? 2 : 4, 1, 1};
-  const int widest = t.mb == 1 ? 2 : 4;
-  while (t.c < widest && tiles_of(M, N, 16 * t.mb, 32 * t.c) >= 192) t.c *= 2;
+  const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  StagedShape best{mb, 1, 1, 1e30};
+  for (int c = 1; c <= (mb == 1 ? 2 : 4); c *= 2) {
+    const int at_once = mb == 1 ? 2 * kCus : kCus;
+    const double round = mb == 1 ? (c == 1 ? 1.0 : 1.8) : c == 1 ? 4.0 : c == 2 ? 5.0 : 7.5;
+    const double us = round * (double)((tiles_of(M, N, 16 * mb, 16 * c) + at_once - 1) / at_once);
+    if (us < best.us) best = {mb, c, 1, us};
+  }
   // Shares of k where the tiles leave three quarters of the CUs idle and each
-  // has a long way to go: 512 k of every wavefront (a second launch costs 4 us)
-  const long long tiles = tiles_of(M, N, 16 * t.mb, 16 * t.c);
+  // has a long way to go: 512 k of every wavefront (a second launch costs 4 us;
+  // 64 x 14336 x 1024 in shares: 10.4 us, whole: 13.9)
+  const long long tiles = tiles_of(M, N, 16 * mb, 16 * best.c);
   if (tiles <= kCus / 4) {
     const long long room = kCus / tiles, work = K / 2048;
-    t.splits = (int)(room < work ? room : work);
-    if (t.splits < 3) t.splits = 1;
+    best.splits = (int)(room < work ? room : work);
+    if (best.splits < 3) best.splits = 1;
   }
-  return t;
+  return best;
+}
+
+enum Kind { kStaged, kMid, kBig };
+Kind kind_of(int M, int K, int N) {
+  auto rounds = [&](int t) { return (double)((tiles_of(M, N, t, t) + kCus - 1) / kCus); };
+  const double staged = staged_shape(M, K, N).us, mid = 21.0 * rounds(kMM), big = 40.0 * rounds(kBM);
+  if (M <= 64 || (staged <= mid && staged <= big)) return kStaged;
+  return mid < big ? kMid : kBig;
 }
 
 size_t staged_bytes(const StagedShape &t, int M, int N) {
@@ -993,7 +1030,7 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
   // rows that direct-to-LDS copies can take
   const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
                        a.ldw % 16 == 0;
-  if (!aligned) {
+  if (!aligned || a.K < 16) {
     // rows at any byte: the loads straight into registers up to 256 rows, above
     // that tiles shared in LDS (777 x 1536 x 4099: 34 us both)
     if (a.K >= 16 && a.M <= 16) return launch_direct<Ty, 1, 1, 8>(a, s);
@@ -1003,7 +1040,7 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
                        dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const Kind kind = kind_of(a.M, a.N);
+  const Kind kind = kind_of(a.M, a.K, a.N);
   if (kind == kStaged) {
     StagedShape t = staged_shape(a.M, a.K, a.N);
     if (!a.ws) t.splits = 1;
@@ -1021,7 +1058,7 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
            : t.c == 2 ? launch_staged<Ty, 4, 2, 4, 2, 8>(a, t.splits, s)
                       : launch_staged<Ty, 4, 4, 4, 2, 8>(a, t.splits, s);
   }
-  if (kind == kMid && a.K >= 16) {
+  if (kind == kMid) {
     const TileOrder order{(a.M + kMM - 1) / kMM, (a.N + kMN - 1) / kMN};
     const long long tiles = (long long)order.ntm * order.ntn;
     hipLaunchKernelGGL(int8_mid_kernel<Ty>, dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)),
@@ -1039,7 +1076,7 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
 }  // namespace
 
 size_t int8_workspace_bytes(int M, int K, int N) {
-  if (kind_of(M, N) != kStaged) return 0;
+  if (kind_of(M, K, N) != kStaged) return 0;
   return staged_bytes(staged_shape(M, K, N), M, N);
 }
 

@@ -69,10 +69,10 @@ __device__ __forceinline__ void load_values(const void *base, long long row_at, 
 // s all 2^(s+1) lanes hold the same, so mirrored lanes serve as partners.
 template <int kStep>
 __device__ __forceinline__ int lane_partner(int x) {
-  if constexpr (kStep == 0) return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);
-  else if constexpr (kStep == 1) return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);
-  else if constexpr (kStep == 2) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);
-  else if constexpr (kStep == 3) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false);
+  if constexpr (kStep == 0) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);
+  else if constexpr (kStep == 1) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);
+  else if constexpr (kStep == 2) return __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);
+  else if constexpr (kStep == 3) return __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);
   else return __shfl_xor(x, 1 << kStep);
 }
 template <int kStep>
@@ -143,19 +143,26 @@ __device__ __forceinline__ int id_of(double k) {
 
 // 2^t for t <= 1000, about 2^-45 of the value: Chebyshev interpolation of
 // degree 9 on [-1/2, 1/2].
+__device__ __forceinline__ double fma_const(double p, double r, double c) {
+  // the constant stays in scalar registers (the compiler's choice copies it into
+  // the result's vector registers first, at every use)
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(p), "v"(r), "s"(c));
+  return d;
+}
 __device__ __forceinline__ double exp2_poly(double t) {
   const double n = __builtin_rint(t);
   const double r = t - n;
   double p = 1.0205905373362123e-07;
-  p = fma(p, r, 1.3259645246593194e-06);
-  p = fma(p, r, 1.525267292505434e-05);
-  p = fma(p, r, 0.0001540343375123525);
-  p = fma(p, r, 0.0013333558200794313);
-  p = fma(p, r, 0.009618129193934349);
-  p = fma(p, r, 0.05550410866465167);
-  p = fma(p, r, 0.2402265069564034);
-  p = fma(p, r, 0.6931471805599462);
-  p = fma(p, r, 1.0000000000000135);
+  p = fma_const(p, r, 1.3259645246593194e-06);
+  p = fma_const(p, r, 1.525267292505434e-05);
+  p = fma_const(p, r, 0.0001540343375123525);
+  p = fma_const(p, r, 0.0013333558200794313);
+  p = fma_const(p, r, 0.009618129193934349);
+  p = fma_const(p, r, 0.05550410866465167);
+  p = fma_const(p, r, 0.2402265069564034);
+  p = fma_const(p, r, 0.6931471805599462);
+  p = fma_const(p, r, 1.0000000000000135);
   return ldexp(p, (int)n);
 }
 constexpr double kLog2e = 1.4426950408889634;
@@ -836,13 +843,25 @@ hipError_t backward_with(const RouteBwdArgs &a, int dtype, hipStream_t s) {
 
 }  // namespace
 
+// Lanes and keys per lane.  Few tokens: four keys, the shortest way through the
+// lane's sort (64 tokens of 256 experts 4.9 us, with eight keys 5.8).  From a
+// wavefront on every SIMD on, eight: fewer lanes repeat the merges (16384 tokens
+// of 128 experts: 5.5 us, with four 8.3).  From 8192 tokens on sixteen (16384
+// tokens of 256 experts in groups: 15.0 us, with eight 16.7, with four 24.2;
+// 4096 of 128: 5.1 with eight and sixteen).
 hipError_t launch_route_topk(const RouteArgs &a, int dtype, hipStream_t s) {
+  constexpr int kWaves = 1024;                       // SIMDs of the card
   if (a.E <= 8) return route_with<8, 1>(a, dtype, s);
   if (a.E <= 32) return route_with<8, 4>(a, dtype, s);
   if (a.E <= 64) return route_with<8, 8>(a, dtype, s);
-  if (a.E <= 128) return route_with<16, 8>(a, dtype, s);
-  if (a.E <= 256) return route_with<32, 8>(a, dtype, s);
-  return route_with<64, 8>(a, dtype, s);
+  const bool few = (long long)a.M * (a.E <= 128 ? 32 : 64) <= 64 * kWaves, many = a.M >= 8192;
+  if (a.E <= 128)
+    return few ? route_with<32, 4>(a, dtype, s)
+               : many ? route_with<8, 16>(a, dtype, s) : route_with<16, 8>(a, dtype, s);
+  if (a.E <= 256)
+    return few ? route_with<64, 4>(a, dtype, s)
+               : many ? route_with<16, 16>(a, dtype, s) : route_with<32, 8>(a, dtype, s);
+  return many ? route_with<32, 16>(a, dtype, s) : route_with<64, 8>(a, dtype, s);
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, int dtype, hipStream_t s) {

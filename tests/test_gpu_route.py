@@ -166,6 +166,26 @@ def test_route_empty_and_large():
     assert np.all(np.sort(ids, 1)[:, 1:] > np.sort(ids, 1)[:, :-1])
 
 
+@pytest.mark.parametrize("M", [1500, 8200])
+@pytest.mark.parametrize("E,n,keep", [(128, 8, 4), (120, 5, 2), (256, 8, 4), (250, 10, 3), (512, 16, 5)])
+def test_route_many_tokens(M, E, n, keep):
+    """The variants with more keys a lane, sampled rows against the oracle."""
+    print(f"\n[route] many M={M} E={E}", flush=True)
+    x = _logits(M, E, "f32", _seed(M, E))
+    x[5, 1::2] = float("-inf")
+    b = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(2))).to(DEV)
+    b[::7] = float("-inf")
+    rows = np.r_[0:30, M // 2:M // 2 + 20, M - 30:M]
+    xs = x.cpu().numpy()[rows]
+    for k in (2, 8):
+        for bias, score, groups, rule in ((b, 1, n, 1), (None, 0, 1, 0), (b, 0, n, 0), (None, 1, n, 1)):
+            ids, w = route(x, "f32", k, bias, score, groups, keep if groups > 1 else 1, rule, True, 2.5)
+            ids0, w0 = L.route_general(xs, None if bias is None else b.cpu().numpy(), k, score, groups,
+                                       keep if groups > 1 else 1, rule, True, 2.5)
+            assert np.array_equal(ids[rows], ids0)
+            assert np.all(np.abs(w[rows] - w0) <= 2.0 ** -23 * w0)
+
+
 # ---- gradient ----------------------------------------------------------------------
 def _dense_tol(x, ids, g, scale):
     """Bound for the dense softmax gradient in float32.  p = exp(x - m) / Z:
