@@ -47,14 +47,14 @@ __device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
   return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
 }
 
-// Any row distance, address and K: 64 x 64 tiles, four wavefronts of 32 x 32
-// (v_mfma_i32_32x32x32_i8, weights as the first operand), 64 k a stage through
-// registers into LDS rows of 80 bytes.
-constexpr int kAnyRow = 80;
-constexpr long long kAnyGrid = 1 << 20;
+// K below 16 (the kernels below move 16 bytes of a row at a time): 64 x 64 tiles,
+// four wavefronts of 32 x 32, byte by byte into LDS rows of 80 bytes, one product
+// of 32 k (v_mfma_i32_32x32x32_i8, weights as the first operand).
+constexpr int kShortRow = 80;
+constexpr long long kShortGrid = 1 << 20;
 template <typename Ty>
-__global__ __launch_bounds__(256) void int8_any_kernel(const Int8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[64 * kAnyRow], s_w[64 * kAnyRow];
+__global__ __launch_bounds__(256) void int8_short_kernel(const Int8Args p) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_a[64 * kShortRow], s_w[64 * kShortRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = tid >> 2, c = (tid & 3) * 16;        // this thread's row and chunk of a stage
   const int g = lane >> 5, q = lane & 31;
@@ -73,13 +73,13 @@ __global__ __launch_bounds__(256) void int8_any_kernel(const Int8Args p) {
       const i32x4 av = am ? load16(ar, k + c, p.K) : z;
       const i32x4 wv = wn ? load16(wr, k + c, p.K) : z;
       __syncthreads();
-      *reinterpret_cast<i32x4 *>(s_a + r * kAnyRow + c) = av;
-      *reinterpret_cast<i32x4 *>(s_w + r * kAnyRow + c) = wv;
+      *reinterpret_cast<i32x4 *>(s_a + r * kShortRow + c) = av;
+      *reinterpret_cast<i32x4 *>(s_w + r * kShortRow + c) = wv;
       __syncthreads();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_a + (mw + q) * kAnyRow + 32 * h + 16 * g);
-        const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_w + (nw + q) * kAnyRow + 32 * h + 16 * g);
+        const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_a + (mw + q) * kShortRow + 32 * h + 16 * g);
+        const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_w + (nw + q) * kShortRow + 32 * h + 16 * g);
         acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, fa, acc, 0, 0, 0);
       }
     }
@@ -425,13 +425,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
   wait_dma_all();                                     // no copy into LDS outlives the workgroup
 }
 
-// ---- few rows: weights straight into registers ------------------------------------
-// One workgroup of kW wavefronts per 16 MB rows x 16 C columns.  The wavefronts
-// share out the contraction (128 k each in turn), load both operands' MFMA
-// fragments straight from memory (any alignment), two such steps ahead, and add
-// their exact partial sums through LDS at the end.  No barrier and no LDS until
-// then, so the loads of every wavefront are always under way: what a weight-bound
-// product needs.
+// ---- few rows: weights through each wavefront's own LDS ----------------------------
+// Four output columns of a row from their exact sums.
 template <typename Ty>
 __device__ __forceinline__ void store_four(const Int8Args &p, int m, int n, float sa, const float *sw,
                                            const float *bias, const i32x4 &sum) {
@@ -469,123 +464,34 @@ __device__ __forceinline__ void store_four(const Int8Args &p, int m, int n, floa
   }
 }
 
-template <typename Ty, int MB, int C, int kW>
-__global__ __launch_bounds__(64 * kW) void int8_direct_kernel(const Int8Args p, int col_tiles) {
-  constexpr int kStep = 128;                          // k of a wavefront's step: whole lines
-  __shared__ __attribute__((aligned(16))) i32x4 s_part[kW][MB * C][64];
-  __shared__ float s_sa[16 * MB], s_sw[16 * C], s_bias[16 * C];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g = lane >> 4, r16 = lane & 15;
-  const int m0 = (blockIdx.x / col_tiles) * (16 * MB), n0 = (blockIdx.x % col_tiles) * (16 * C);
-  for (int i = tid; i < 16 * C; i += 64 * kW) {
-    s_sw[i] = p.w_scale[min(n0 + i, p.N - 1)];
-    if (p.bias) s_bias[i] = p.bias[min(n0 + i, p.N - 1)];
-  }
-  for (int i = tid; i < 16 * MB; i += 64 * kW) s_sa[i] = p.a_scale[min(m0 + i, p.M - 1)];
-
-  // rows past the last repeat it; their results are not stored
-  const int8_t *a0 = p.a + (long long)m0 * p.lda, *w0 = p.w + (long long)n0 * p.ldw;
-  uint32_t a_off[MB], w_off[C];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-    a_off[i] = (uint32_t)min(16 * i + r16, p.M - 1 - m0) * (uint32_t)p.lda + 16u * g;
-#pragma unroll
-  for (int j = 0; j < C; ++j)
-    w_off[j] = (uint32_t)min(16 * j + r16, p.N - 1 - n0) * (uint32_t)p.ldw + 16u * g;
-
-  i32x4 acc[MB][C];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
-  struct Step {
-    i32x4 a[MB][2], w[C][2];
-  };
-  auto load = [&](Step &f, int k0) QMOE_INLINE {
-    if (k0 + kStep <= p.K) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) __builtin_memcpy(&f.w[j][c], w0 + k0 + 64 * c + w_off[j], 16);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) __builtin_memcpy(&f.a[i][c], a0 + k0 + 64 * c + a_off[i], 16);
-      }
-    } else if (k0 < p.K) {                            // the last bytes of the rows
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = k0 + 64 * c + 16 * g;
-#pragma unroll
-        for (int j = 0; j < C; ++j) f.w[j][c] = load_end(w0 + w_off[j] - 16 * g, k, p.K);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) f.a[i][c] = load_end(a0 + a_off[i] - 16 * g, k, p.K);
-      }
-    }
-  };
-  auto multiply = [&](const Step &f) QMOE_INLINE {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[j][c], f.a[i][c], acc[i][j], 0, 0, 0);
-  };
-  // this wavefront's steps wave, wave + kW, ..; every workgroup begins at another
-  const int n = ((p.K + kStep - 1) / kStep - wave + kW - 1) / kW;
-  Step f0, f1;
-  int at = n > 0 ? (int)(blockIdx.x / kXcds) % n : 0;
-  auto next = [&]() QMOE_INLINE -> int {
-    const int k = (at * kW + wave) * kStep;
-    at = at + 1 < n ? at + 1 : 0;
-    return k;
-  };
-  if (n > 0) load(f0, next());
-  if (n > 1) load(f1, next());
-  for (int i = 0; i < n; i += 2) {
-    multiply(f0);
-    if (i + 2 < n) load(f0, next());
-    if (i + 1 >= n) break;
-    multiply(f1);
-    if (i + 3 < n) load(f1, next());
-  }
-
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < C; ++j) s_part[wave][i * C + j][lane] = acc[i][j];
-  __syncthreads();
-  for (int f = wave; f < MB * C; f += kW) {
-    i32x4 sum = s_part[0][f][lane];
-#pragma unroll
-    for (int w = 1; w < kW; ++w) sum += s_part[w][f][lane];
-    const int i = f / C, col = 16 * (f - i * C) + 4 * g;
-    store_four<Ty>(p, m0 + 16 * i + r16, n0 + col, s_sa[16 * i + r16], s_sw + col, s_bias + col, sum);
-  }
-}
-
-// ---- few rows, aligned: weights through each wavefront's own LDS ----------------------
-// As int8_direct_kernel, but a step's rows come as whole 128-byte lines by
-// direct-to-LDS DMA into the wavefront's own ring of kD steps, from where the
-// fragments are read.  (A fragment's 64 lanes read 16 rows, neighbouring lanes in
-// different rows: straight from memory that is 64 line look-ups for 1 KB, and the
-// cache's look-ups bound the kernel.)  A wavefront waits only for its own copies.
+// One workgroup of kW wavefronts per 16 MB rows x 16 C columns.  The wavefronts
+// share out the contraction, 128 k each in turn, and add their exact partial sums
+// through LDS at the end; until then each waits for nothing but its own loads, so
+// those are always under way: what a weight-bound product needs.
+//
+// A step's rows come as whole 128-byte lines, neighbouring lanes neighbouring
+// chunks, into the wavefront's own part of LDS, from where the fragments are read.
+// (Loaded straight into fragments, neighbouring lanes are in different rows: 64
+// line look-ups for 1 KB, and the cache's look-ups bound the kernel; 64 x 4096 x
+// 14336: 18.6 us, 12.9 this way.)  With kDma the copies go to LDS directly, kD
+// steps ahead, which needs rows on 16 bytes; without, they pass through registers,
+// two steps ahead, and rows may begin at any byte.
 // AI: copies of activation rows a step, 8 rows each.
 // With `splits` > 1, workgroup (tile, y) contracts the y-th share of k and leaves
 // its sums in p.ws for int8_join_kernel.
 __device__ __forceinline__ int padded_cols(int N) { return (N + 3) & ~3; }
 
-template <typename Ty, int MB, int C, int kW, int kD, int AI>
+template <typename Ty, int MB, int C, int kW, int kD, int AI, bool kDma>
 __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, int col_tiles,
                                                               int splits) {
   constexpr int kStep = 128, kRows = 16 * (MB + C), kSlot = kRows * kStep;
   constexpr int kPieces = AI + 2 * C;
-  constexpr int kRingBytes = kW * kD * kSlot, kPartBytes = kW * MB * C * 1024;
-  static_assert((kD - 1) * kPieces < 64, "the copies in flight are counted in 6 bits");
+  constexpr int kSlots = kDma ? kD : 1;
+  constexpr int kRingBytes = kW * kSlots * kSlot, kPartBytes = kW * MB * C * 1024;
+  static_assert(!kDma || (kD - 1) * kPieces < 64, "the copies in flight are counted in 6 bits");
   __shared__ __attribute__((aligned(1024))) uint8_t
       s_ring[kRingBytes > kPartBytes ? kRingBytes : kPartBytes];   // the partial sums reuse it
-  __shared__ __attribute__((aligned(1024))) uint8_t s_end[kSlot];    // a last, shorter step
+  __shared__ __attribute__((aligned(1024))) uint8_t s_end[kDma ? kSlot : 16];  // a last, shorter step
   __shared__ float s_sa[16 * MB], s_sw[16 * C], s_bias[16 * C];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -607,7 +513,7 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
     w_off[u] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.ldw +
                16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
   }
-  uint8_t *mine = s_ring + wave * kD * kSlot;
+  uint8_t *mine = s_ring + wave * kSlots * kSlot;
   const uint32_t ring = lds_addr(mine);
   auto copy = [&](int slot, int k0) QMOE_INLINE {
     const uint32_t at = ring + (uint32_t)(slot * kSlot);
@@ -626,7 +532,9 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
   // this wavefront's whole steps turn, turn + turns, ..; every workgroup begins at
   // another (a few percent where they all run through the same lines of k)
   const int turn = (int)blockIdx.y * kW + wave, turns = splits * kW;
-  const int whole = p.K / kStep, n = (whole - turn + turns - 1) / turns;
+  const int whole = p.K / kStep;
+  const int steps = kDma ? whole : (p.K + kStep - 1) / kStep;        // with registers the last too
+  const int n = (steps - turn + turns - 1) / turns;
   int at = n > 0 ? (int)(blockIdx.x / kXcds) % n : 0;
   auto next = [&]() QMOE_INLINE -> int {
     const int k = (at * turns + turn) * kStep;
@@ -638,7 +546,7 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
   // masked below).
   const int end = whole * kStep, chunks = (p.K - end) / 16, rest = (p.K - end) & 15;
   const bool ends = whole % turns == turn;
-  if (ends && chunks > 0) {
+  if (kDma && ends && chunks > 0) {
     const uint32_t at_end = lds_addr(s_end);
 #pragma unroll
     for (int u = 0; u < 2 * C; ++u) {
@@ -652,9 +560,45 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
       dma16(a0 + end, a_off[u] - 16u * (uint32_t)max(0, c - (chunks - 1)), at_end + (uint32_t)(u * 1024));
     }
   }
+  // without kDma: a step's rows on their way to LDS
+  struct Rows {
+    i32x4 a[AI], w[2 * C];
+  };
+  auto fetch = [&](Rows &x, int k0) QMOE_INLINE {
+    if (k0 + kStep <= p.K) {
 #pragma unroll
-  for (int d = 0; d < kD; ++d)
-    if (d < n) copy(d, next());
+      for (int u = 0; u < 2 * C; ++u) __builtin_memcpy(&x.w[u], w0 + k0 + w_off[u], 16);
+#pragma unroll
+      for (int u = 0; u < AI; ++u) __builtin_memcpy(&x.a[u], a0 + k0 + a_off[u], 16);
+    } else {                                          // zero past K
+#pragma unroll
+      for (int u = 0; u < 2 * C; ++u) {
+        const int c = 16 * ((lane & 7) ^ (((8 * u + (lane >> 3)) >> 1) & 7));
+        x.w[u] = load_end(w0 + w_off[u] - c, k0 + c, p.K);
+      }
+#pragma unroll
+      for (int u = 0; u < AI; ++u) {
+        const int c = 16 * ((lane & 7) ^ (((8 * u + (lane >> 3)) >> 1) & 7));
+        x.a[u] = load_end(a0 + a_off[u] - c, k0 + c, p.K);
+      }
+    }
+  };
+  auto put = [&](const Rows &x) QMOE_INLINE {
+#pragma unroll
+    for (int u = 0; u < 2 * C; ++u)
+      *reinterpret_cast<i32x4 *>(mine + 16 * MB * kStep + u * 1024 + lane * 16) = x.w[u];
+#pragma unroll
+    for (int u = 0; u < AI; ++u) *reinterpret_cast<i32x4 *>(mine + u * 1024 + lane * 16) = x.a[u];
+  };
+  Rows x0, x1;
+  if constexpr (kDma) {
+#pragma unroll
+    for (int d = 0; d < kD; ++d)
+      if (d < n) copy(d, next());
+  } else {
+    if (n > 0) fetch(x0, next());
+    if (n > 1) fetch(x1, next());
+  }
   // scales and bias, behind the first copies
   float side = 0.0f, side2 = 0.0f;
   const int q = tid - 16 * C;
@@ -687,39 +631,57 @@ __global__ __launch_bounds__(64 * kW) void int8_staged_kernel(const Int8Args p, 
       for (int i = 0; i < MB; ++i)
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j][c], fa[i][c], acc[i][j], 0, 0, 0);
   };
-  int slot = 0;
-  for (int i = 0; i < n; ++i) {
-    if (i + kD <= n) wait_dma<(kD - 1) * kPieces>();
-    else wait_dma_all();
-    read(mine + slot * kSlot);
-    wait_lds();                                       // the slot has been read
-    if (i + kD < n) copy(slot, next());
-    multiply(0);
-    multiply(1);
-    slot = slot + 1 < kD ? slot + 1 : 0;
-  }
-  if (ends && chunks > 0) {
-    wait_dma_all();
-    read(s_end);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        if (4 * c + g >= chunks) fa[i][c] = i32x4{0, 0, 0, 0};
-      multiply(c);
+  if constexpr (kDma) {
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+      if (i + kD <= n) wait_dma<(kD - 1) * kPieces>();
+      else wait_dma_all();
+      read(mine + slot * kSlot);
+      wait_lds();                                     // the slot has been read
+      if (i + kD < n) copy(slot, next());
+      multiply(0);
+      multiply(1);
+      slot = slot + 1 < kD ? slot + 1 : 0;
     }
-  }
-  if (ends && rest > 0) {                             // the last bytes, straight from memory
-    const int k = p.K - rest;
+    if (ends && chunks > 0) {
+      wait_dma_all();
+      read(s_end);
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      fw[j][0] = load_end(w0 + (long long)min(16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      fa[i][0] = load_end(a0 + (long long)min(16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
-      if (g > 0) fa[i][0] = i32x4{0, 0, 0, 0};
+        for (int i = 0; i < MB; ++i)
+          if (4 * c + g >= chunks) fa[i][c] = i32x4{0, 0, 0, 0};
+        multiply(c);
+      }
     }
-    multiply(0);
+    if (ends && rest > 0) {                           // the last bytes, straight from memory
+      const int k = p.K - rest;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        fw[j][0] = load_end(w0 + (long long)min(16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        fa[i][0] = load_end(a0 + (long long)min(16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
+        if (g > 0) fa[i][0] = i32x4{0, 0, 0, 0};
+      }
+      multiply(0);
+    }
+  } else {
+    // a wavefront's LDS accesses are carried out in order: no barrier between its
+    // writes and reads
+    auto step = [&](Rows &x, int i) QMOE_INLINE {
+      put(x);
+      if (i + 2 < n) fetch(x, next());
+      wait_lds();
+      read(mine);
+      wait_lds();
+      multiply(0);
+      multiply(1);
+    };
+    for (int i = 0; i < n; i += 2) {
+      step(x0, i);
+      if (i + 1 < n) step(x1, i + 1);
+    }
   }
 
   if (tid < 16 * C) {
@@ -954,30 +916,36 @@ long long tiles_of(int M, int N, int tm, int tn) {
 }
 
 // The kernels and their tiles, by the time they take: rounds of one workgroup a CU
-// (two for the smallest), each as long as measured at K = 4096; all grow with K
-// alike, so the least time by that count wins.
-//
-// int8_staged_kernel, 16, 32 or 64 columns: a round of 4, 5, 7.5 us (64 x 4096 x
-// 4096: 6.4, 7.3, 9.7 us with the launch; 64 x 4096 x 14336: 20.5, 14.5, 12.9).
-// With up to 16 rows two workgroups fit a CU, 1 or 1.8 us a round of those (1 x
-// 4096 x 14336: 11.0 us with 16 columns, 10.3 with 32).
-// 128 x 128 tiles (int8_mid_kernel): 21 us; 256 x 256 (int8_big_kernel): 40 us.
-// On both sides of the borders (us, staged / mid / big, M x K x N): 512 x 4096 x
-// 4096 19 / 21 / 38, 1024 x 4096 x 4096 36 / 25 / 39, 2048 x 4096 x 4096 69 / 47
-// / 40, 512 x 4096 x 14336 73 / 45 / 40.
+// (of two for up to 16 rows), each a fixed part and one that grows with K, in us
+// for K = 4096, fitted to measured calls.  The least by that count wins.
+//   int8_staged_kernel, 64 rows: 16, 32, 64 columns 1.5 + 2.5, 2 + 3, 3.2 + 5.6
+//     (64 x 4096 x 4096: 6.4, 7.3, 9.7 with the launch; 64 x 4096 x 14336: 20.5,
+//     14.5, 12.9); up to 16 rows: 16, 32 columns 0.6 + 0.5, 0.9 + 0.9 (1 x 4096 x
+//     14336: 11.0, 10.3)
+//   int8_mid_kernel 2.7 + 18, int8_big_kernel 5.5 + 33
+// On both sides of the borders (us, staged / mid / big, M x K x N): 512 x 2048 x
+// 4096 14.0 / 13.1 / 23.3, 512 x 4096 x 4096 19.9 / 20.4 / 38.1, 200 x 512 x 16384
+// 16.2 / 8.2 / 11.9, 1024 x 64 x 8192 30.4 / 10.1 / 9.9, 1024 x 2048 x 8192 52.1 /
+// 29.5 / 25.0, 732 x 7872 x 7168 104.8 / 81.5 / 79.1.
 constexpr int kCus = 256;
+struct Cost {
+  double fixed, at_4096;
+  double of(long long tiles, int at_once, int K) const {
+    return (double)((tiles + at_once - 1) / at_once) * (fixed + at_4096 * K / 4096.0);
+  }
+};
 struct StagedShape {
   int mb, c, splits;                                  // 16 mb rows, 16 c columns, shares of k
-  double us;                                          // at K = 4096
+  double us;
 };
 StagedShape staged_shape(int M, int K, int N) {
+  constexpr Cost kFew[2] = {{0.6, 0.5}, {0.9, 0.9}}, kMore[3] = {{1.5, 2.5}, {2.0, 3.0}, {3.2, 5.6}};
   const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  StagedShape best{mb, 1, 1, 1e30};
-  for (int c = 1; c <= (mb == 1 ? 2 : 4); c *= 2) {
-    const int at_once = mb == 1 ? 2 * kCus : kCus;
-    const double round = mb == 1 ? (c == 1 ? 1.0 : 1.8) : c == 1 ? 4.0 : c == 2 ? 5.0 : 7.5;
-    const double us = round * (double)((tiles_of(M, N, 16 * mb, 16 * c) + at_once - 1) / at_once);
-    if (us < best.us) best = {mb, c, 1, us};
+  StagedShape best{mb, 1, 1, 1e300};
+  for (int i = 0; i < (mb == 1 ? 2 : 3); ++i) {
+    const long long tiles = tiles_of(M, N, 16 * mb, 16 << i);
+    const double us = mb == 1 ? kFew[i].of(tiles, 2 * kCus, K) : kMore[i].of(tiles, kCus, K);
+    if (us < best.us) best = {mb, 1 << i, 1, us};
   }
   // Shares of k where the tiles leave three quarters of the CUs idle and each
   // has a long way to go: 512 k of every wavefront (a second launch costs 4 us;
@@ -993,9 +961,11 @@ StagedShape staged_shape(int M, int K, int N) {
 
 enum Kind { kStaged, kMid, kBig };
 Kind kind_of(int M, int K, int N) {
-  auto rounds = [&](int t) { return (double)((tiles_of(M, N, t, t) + kCus - 1) / kCus); };
-  const double staged = staged_shape(M, K, N).us, mid = 21.0 * rounds(kMM), big = 40.0 * rounds(kBM);
-  if (M <= 64 || (staged <= mid && staged <= big)) return kStaged;
+  constexpr Cost kMidCost{2.7, 18.0}, kBigCost{5.5, 33.0};
+  const double staged = staged_shape(M, K, N).us;
+  const double mid = kMidCost.of(tiles_of(M, N, kMM, kMN), kCus, K);
+  const double big = kBigCost.of(tiles_of(M, N, kBM, kBN), kCus, K);
+  if (staged <= mid && staged <= big) return kStaged;
   return mid < big ? kMid : kBig;
 }
 
@@ -1003,10 +973,11 @@ size_t staged_bytes(const StagedShape &t, int M, int N) {
   return t.splits == 1 ? 0 : (size_t)t.splits * M * ((N + 3) / 4 * 4) * sizeof(int);
 }
 
-template <typename Ty, int MB, int C, int kW, int kD, int AI>
+template <typename Ty, int MB, int C, int kD, int AI, bool kDma>
 hipError_t launch_staged(const Int8Args &a, int splits, hipStream_t s) {
+  constexpr int kW = 4;
   const int cols = (a.N + 16 * C - 1) / (16 * C), rows = (a.M + 16 * MB - 1) / (16 * MB);
-  hipLaunchKernelGGL((int8_staged_kernel<Ty, MB, C, kW, kD, AI>),
+  hipLaunchKernelGGL((int8_staged_kernel<Ty, MB, C, kW, kD, AI, kDma>),
                      dim3((unsigned)(cols * rows), (unsigned)splits), dim3(64 * kW), 0, s, a, cols,
                      splits);
   const hipError_t e = hipGetLastError();
@@ -1017,47 +988,38 @@ hipError_t launch_staged(const Int8Args &a, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename Ty, int MB, int C, int kW>
-hipError_t launch_direct(const Int8Args &a, hipStream_t s) {
-  const int cols = (a.N + 16 * C - 1) / (16 * C), rows = (a.M + 16 * MB - 1) / (16 * MB);
-  hipLaunchKernelGGL((int8_direct_kernel<Ty, MB, C, kW>), dim3((unsigned)(cols * rows)), dim3(64 * kW),
-                     0, s, a, cols);
-  return hipGetLastError();
+template <typename Ty, bool kDma>
+hipError_t launch_staged_shape(const Int8Args &a, StagedShape t, hipStream_t s) {
+  if (!a.ws) t.splits = 1;
+  if (t.mb == 1 && t.c == 1)
+    return a.M <= 8 ? launch_staged<Ty, 1, 1, 4, 1, kDma>(a, t.splits, s)
+                    : launch_staged<Ty, 1, 1, 4, 2, kDma>(a, t.splits, s);
+  if (t.mb == 1)
+    return a.M <= 8 ? launch_staged<Ty, 1, 2, 3, 1, kDma>(a, t.splits, s)
+                    : launch_staged<Ty, 1, 2, 3, 2, kDma>(a, t.splits, s);
+  if (t.mb == 2)
+    return t.c == 1   ? launch_staged<Ty, 2, 1, 4, 4, kDma>(a, t.splits, s)
+           : t.c == 2 ? launch_staged<Ty, 2, 2, 4, 4, kDma>(a, t.splits, s)
+                      : launch_staged<Ty, 2, 4, 3, 4, kDma>(a, t.splits, s);
+  return t.c == 1   ? launch_staged<Ty, 4, 1, 2, 8, kDma>(a, t.splits, s)
+         : t.c == 2 ? launch_staged<Ty, 4, 2, 2, 8, kDma>(a, t.splits, s)
+                    : launch_staged<Ty, 4, 4, 2, 8, kDma>(a, t.splits, s);
 }
 
 template <typename Ty>
 hipError_t launch(const Int8Args &a, hipStream_t s) {
-  // rows that direct-to-LDS copies can take
-  const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
-                       a.ldw % 16 == 0;
-  if (!aligned || a.K < 16) {
-    // rows at any byte: the loads straight into registers up to 256 rows, above
-    // that tiles shared in LDS (777 x 1536 x 4099: 34 us both)
-    if (a.K >= 16 && a.M <= 16) return launch_direct<Ty, 1, 1, 8>(a, s);
-    if (a.K >= 16 && a.M <= 256) return launch_direct<Ty, 4, 2, 4>(a, s);
+  if (a.K < 16) {
     const long long tiles = tiles_of(a.M, a.N, 64, 64);
-    hipLaunchKernelGGL(int8_any_kernel<Ty>, dim3((unsigned)(tiles < kAnyGrid ? tiles : kAnyGrid)),
+    hipLaunchKernelGGL(int8_short_kernel<Ty>, dim3((unsigned)(tiles < kShortGrid ? tiles : kShortGrid)),
                        dim3(256), 0, s, a);
     return hipGetLastError();
   }
+  // rows that direct-to-LDS copies can take
+  const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
+                       a.ldw % 16 == 0;
+  if (!aligned) return launch_staged_shape<Ty, false>(a, staged_shape(a.M, a.K, a.N), s);
   const Kind kind = kind_of(a.M, a.K, a.N);
-  if (kind == kStaged) {
-    StagedShape t = staged_shape(a.M, a.K, a.N);
-    if (!a.ws) t.splits = 1;
-    if (t.mb == 1 && t.c == 1)
-      return a.M <= 8 ? launch_staged<Ty, 1, 1, 4, 4, 1>(a, t.splits, s)
-                      : launch_staged<Ty, 1, 1, 4, 4, 2>(a, t.splits, s);
-    if (t.mb == 1)
-      return a.M <= 8 ? launch_staged<Ty, 1, 2, 4, 3, 1>(a, t.splits, s)
-                      : launch_staged<Ty, 1, 2, 4, 3, 2>(a, t.splits, s);
-    if (t.mb == 2)
-      return t.c == 1   ? launch_staged<Ty, 2, 1, 4, 4, 4>(a, t.splits, s)
-             : t.c == 2 ? launch_staged<Ty, 2, 2, 4, 4, 4>(a, t.splits, s)
-                        : launch_staged<Ty, 2, 4, 4, 3, 4>(a, t.splits, s);
-    return t.c == 1   ? launch_staged<Ty, 4, 1, 4, 2, 8>(a, t.splits, s)
-           : t.c == 2 ? launch_staged<Ty, 4, 2, 4, 2, 8>(a, t.splits, s)
-                      : launch_staged<Ty, 4, 4, 4, 2, 8>(a, t.splits, s);
-  }
+  if (kind == kStaged) return launch_staged_shape<Ty, true>(a, staged_shape(a.M, a.K, a.N), s);
   if (kind == kMid) {
     const TileOrder order{(a.M + kMM - 1) / kMM, (a.N + kMN - 1) / kMN};
     const long long tiles = (long long)order.ntm * order.ntn;
@@ -1067,16 +1029,16 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
   }
   const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};
   const long long tiles = (long long)order.ntm * order.ntn;
-  const int cus = compute_units();
-  hipLaunchKernelGGL(int8_big_kernel<Ty>, dim3((unsigned)(tiles < cus ? tiles : cus)),
-                     dim3(kBigThreads), 0, s, a, order);
+  // a workgroup for every tile of every XCD's run, as far as there are CUs
+  const long long all = (tiles + kXcds - 1) / kXcds * kXcds, cus = compute_units();
+  hipLaunchKernelGGL(int8_big_kernel<Ty>, dim3((unsigned)(all < cus ? all : cus)), dim3(kBigThreads), 0,
+                     s, a, order);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t int8_workspace_bytes(int M, int K, int N) {
-  if (kind_of(M, K, N) != kStaged) return 0;
   return staged_bytes(staged_shape(M, K, N), M, N);
 }
 
