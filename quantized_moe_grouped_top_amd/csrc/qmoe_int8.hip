@@ -735,12 +735,14 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args p, int sp
 // the whole tile (wavefront: 64 x 64 outputs), with its own ring of four 64-k
 // stages, so every SIMD has two wavefronts even where the output has no more
 // tiles than the card CUs.  A stage's fragments are read while the one before is
-// multiplied; one barrier a stage.  The groups' exact sums meet in LDS.
+// multiplied; one barrier a stage.  The groups' exact sums meet in LDS.  Without
+// kDma (rows that begin at any byte) a stage passes through registers: fetched
+// two steps before it is written to LDS, which is one before it is read.
 constexpr int kMM = 128, kMN = 128;
 constexpr int kMidSlot = (kMM + kMN) * kBK;          // 16 KB
 constexpr int kMidPieces = 4;
 
-template <typename Ty>
+template <typename Ty, bool kDma>
 __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, TileOrder order) {
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kRing * kMidSlot];
   __shared__ float s_sa[kMM], s_sw[kMN], s_bias[kMN];
@@ -807,11 +809,41 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[j], f.a[i], acc[i][j], 0, 0, 0);
   };
 
+  struct Rows {
+    i32x4 v[kMidPieces];
+  };
+  auto fetch = [&](Rows &x, int s) QMOE_INLINE {
+    const int k0 = (first + min(s, mine - 1)) * kBK;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      __builtin_memcpy(&x.v[u], a0 + k0 + a_off[u], 16);
+      __builtin_memcpy(&x.v[u + 2], w0 + k0 + w_off[u], 16);
+    }
+  };
+  auto put = [&](const Rows &x, int s) QMOE_INLINE {
+    uint8_t *at = base + (s & (kRing - 1)) * kMidSlot + w4 * 2048 + lane * 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      *reinterpret_cast<i32x4 *>(at + u * 1024) = x.v[u];
+      *reinterpret_cast<i32x4 *>(at + kMM * kBK + u * 1024) = x.v[u + 2];
+    }
+  };
   float side = 0.0f, side2 = 0.0f;
   Frags f0, f1;
+  Rows x0, x1;
   if (mine > 0) {
+    if constexpr (kDma) {
 #pragma unroll
-    for (int s = 0; s < kRing; ++s) copy(s);
+      for (int s = 0; s < kRing; ++s) copy(s);
+    } else {
+      Rows y0, y1;
+      fetch(y0, 0);
+      fetch(y1, 1);
+      fetch(x0, 2);
+      fetch(x1, 3);
+      put(y0, 0);
+      put(y1, 1);
+    }
   }
   if (tid < kMN) {
     side = p.w_scale[min(n0 + tid, p.N - 1)];
@@ -827,13 +859,14 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
   }
   // Stage s + 1 has landed everywhere, and everybody has read stage s, after the
   // barrier of step s; the copies of the two stages behind it may be under way.
-  wait_dma<3 * kMidPieces>();
+  if constexpr (kDma) wait_dma<3 * kMidPieces>();
+  wait_lds();
   phase_end();
   if (mine > 0) read(f0, 0);
   wait_lds();
   // a step's reads and copies go between its products, where they do not hold them up
-  auto step = [&](Frags &now, Frags &then, int s) QMOE_INLINE {
-    wait_dma<2 * kMidPieces>();
+  auto step = [&](Frags &now, Frags &then, Rows &x, int s) QMOE_INLINE {
+    if constexpr (kDma) wait_dma<2 * kMidPieces>();
     phase_end();
     const uint8_t *q = base + ((s + 1) & (kRing - 1)) * kMidSlot;
     const int k0 = (first + min(s + kRing, mine - 1)) * kBK;
@@ -847,6 +880,9 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
           const int r = e >> 1;
           if (r < 4) then.w[r] = *reinterpret_cast<const i32x4 *>(q + w_rd + r * 16 * kBK);
           else then.a[r - 4] = *reinterpret_cast<const i32x4 *>(q + a_rd + (r - 4) * 16 * kBK);
+        } else if (!kDma) {
+          if (e == 1) put(x, s + 2);
+          if (e == 9) fetch(x, s + 4);
         } else if ((e & 3) == 3) {
           const int u = e >> 2;
           if (u < 2) dma16(a0 + k0, a_off[u], at + (uint32_t)(u * 1024));
@@ -858,8 +894,8 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
     wait_lds();
   };
   for (int s = 0; s < steps; s += 2) {
-    step(f0, f1, s);
-    if (s + 1 < steps) step(f1, f0, s + 1);
+    step(f0, f1, x0, s);
+    if (s + 1 < steps) step(f1, f0, x1, s + 1);
   }
   // the last bytes of the rows, straight from memory
   if (grp == 1 && p.K > whole * kBK) {
@@ -1017,14 +1053,16 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
   // rows that direct-to-LDS copies can take
   const bool aligned = ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 && a.lda % 16 == 0 &&
                        a.ldw % 16 == 0;
-  if (!aligned) return launch_staged_shape<Ty, false>(a, staged_shape(a.M, a.K, a.N), s);
   const Kind kind = kind_of(a.M, a.K, a.N);
+  if (!aligned && kind == kStaged)
+    return launch_staged_shape<Ty, false>(a, staged_shape(a.M, a.K, a.N), s);
   if (kind == kStaged) return launch_staged_shape<Ty, true>(a, staged_shape(a.M, a.K, a.N), s);
-  if (kind == kMid) {
+  if (kind == kMid || !aligned) {
     const TileOrder order{(a.M + kMM - 1) / kMM, (a.N + kMN - 1) / kMN};
     const long long tiles = (long long)order.ntm * order.ntn;
-    hipLaunchKernelGGL(int8_mid_kernel<Ty>, dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)),
-                       dim3(512), 0, s, a, order);
+    const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds));
+    if (aligned) hipLaunchKernelGGL((int8_mid_kernel<Ty, true>), grid, dim3(512), 0, s, a, order);
+    else hipLaunchKernelGGL((int8_mid_kernel<Ty, false>), grid, dim3(512), 0, s, a, order);
     return hipGetLastError();
   }
   const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};

@@ -111,6 +111,92 @@ def test_int8_rows(M, K, N):
     check(M, K, N)
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 14336, 256), (3, 12101, 124), (12, 8200, 300), (20, 6160, 96),
+                                   (64, 14336, 1024), (33, 8192, 130), (100, 16384, 64)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_int8_shares_of_k(M, K, N, out):
+    """Shapes whose contraction is shared out through the workspace."""
+    assert qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N) > 0
+    check(M, K, N, out, bias=True, addend=True)
+    check(M, K, N, out, pad=(3, 5, 1), off=(1, 2))
+    check(M, K, N, out, pad=((-K) % 16, (-K) % 16, 0), ws=False)
+
+
+@pytest.mark.parametrize("M,K,N", [(4352, 64, 4352), (4300, 80, 4400), (4352, 40, 4357), (4353, 200, 4352),
+                                   (2500, 336, 9000)])
+def test_int8_several_tiles_a_workgroup(M, K, N):
+    check(M, K, N)
+    check(M, K, N, "f32", bias=True, pad=((-K) % 16, (-K) % 16, 1))
+
+
+@pytest.mark.parametrize("K", [16, 17, 31, 32, 48, 63, 65, 112, 127, 129, 143, 144, 240, 271, 1040])
+def test_int8_ends_of_rows(K):
+    """Every kernel's last, shorter step, in aligned rows and in rows at any byte."""
+    for M, N in [(2, 40), (13, 90), (30, 130), (60, 200), (600, 1100), (1500, 1600)]:
+        check(M, K, N, pad=((-K) % 16, (-K) % 16, 0))
+        check(M, K, N, "f32", pad=(1, 1, 0), off=(1, 1))
+
+
+def test_int8_two_streams():
+    """Two calls at once, each with its own workspace, on two streams."""
+    print("\n[int8] two streams", flush=True)
+    M, K, N = 40, 14336, 512
+    g = _gen("two")
+    outs, refs, keep = [], [], []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(2):
+        a, w = _codes(M, K, K, 0, g), _codes(N, K, K, 0, g)
+        one = torch.ones(max(M, N), device=DEV)
+        ws = torch.empty(qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N), dtype=torch.uint8, device=DEV)
+        ref = torch.empty(M, N, device=DEV)
+        qm.moe_gemm_int8w8a8(a, K, one, w, K, one, None, None, M, K, N, 0, ref, N, None)
+        keep.append((a, w, one, ws))
+        refs.append(ref)
+        outs.append(torch.empty(M, N, device=DEV))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            a, w, one, ws = keep[i]
+            qm.moe_gemm_int8w8a8(a, K, one, w, K, one, None, None, M, K, N, 0, outs[i], N, ws,
+                                 stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], refs[i])
+
+
+def test_int8_kernels_in_a_graph():
+    """The kernels of all sizes captured once and replayed on changing inputs."""
+    print("\n[int8] graph", flush=True)
+    g = _gen("graphs")
+    work = []
+    for M, K, N in [(1, 14336, 256), (64, 512, 1024), (300, 640, 2048), (1200, 256, 3000)]:
+        a, w = _codes(M, K, K, 0, g), _codes(N, K, K, 0, g)
+        sa, sw = torch.rand(M, generator=g).to(DEV), torch.rand(N, generator=g).to(DEV)
+        ws = torch.empty(qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N) + 16, dtype=torch.uint8, device=DEV)
+        work.append((M, K, N, a, w, sa, sw, ws, [torch.zeros(M, N, device=DEV) for _ in range(2)]))
+
+    def step(k):
+        for M, K, N, a, w, sa, sw, ws, y in work:
+            qm.moe_gemm_int8w8a8(a, K, sa, w, K, sw, None, None, M, K, N, 0, y[k], N, ws)
+
+    step(0)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(1)
+    for r in range(3):
+        for M, K, N, a, *_ in work:
+            a.copy_(torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8))
+        step(0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for M, K, N, *_, y in work:
+            assert torch.equal(y[0], y[1]), (r, M, K, N)
+
+
 def test_int8_extreme_codes():
     """All codes -128 at the largest K: the sum 128 * 128 * K is just below 2^31."""
     print("\n[int8] extreme", flush=True)
