@@ -36,15 +36,22 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
 
 // 16 bytes of a row of at least 16 from byte k on, zero past K: the row's last 16
 // bytes moved down.
+__device__ __forceinline__ i32x4 fetch_end(const int8_t *row, int k, int K) {   // as they lie
+  i32x4 v;
+  __builtin_memcpy(&v, row + min(k, K - 16), 16);
+  return v;
+}
+__device__ __forceinline__ i32x4 shift_end(const i32x4 &x, int k, int K) {
+  const int drop = 8 * (k - min(k, K - 16));          // bits
+  const uint64_t a = (uint32_t)x[0] | ((uint64_t)(uint32_t)x[1] << 32);
+  const uint64_t b = (uint32_t)x[2] | ((uint64_t)(uint32_t)x[3] << 32);
+  const uint64_t lo = drop < 64 ? (a >> drop) | (b << 1 << (63 - drop)) : b >> (drop & 63);
+  const uint64_t hi = drop < 64 ? b >> drop : 0;
+  if (k >= K) return i32x4{0, 0, 0, 0};
+  return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+}
 __device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
-  const int at = min(k, K - 16), drop = 8 * (k - at);  // bits
-  uint64_t v[2];
-  __builtin_memcpy(v, row + at, 16);
-  const uint64_t lo = drop < 64 ? (v[0] >> drop) | (v[1] << 1 << (63 - drop)) : v[1] >> (drop & 63);
-  const uint64_t hi = drop < 64 ? v[1] >> drop : 0;
-  v[0] = k < K ? lo : 0;
-  v[1] = k < K ? hi : 0;
-  return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+  return shift_end(fetch_end(row, k, K), k, K);
 }
 
 // K below 16 (the kernels below move 16 bytes of a row at a time): 64 x 64 tiles,
@@ -857,6 +864,18 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
   } else if (tid < kMN + kMM) {
     s_sa[tid - kMN] = side;
   }
+  // the last bytes of the rows, straight from memory: fetched here, used at the end
+  Frags fe;
+  const bool ends = grp == 1 && p.K > whole * kBK;
+  const int ke = whole * kBK + 16 * g;
+  if (ends) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      fe.w[j] = fetch_end(w0 + (long long)min(wn * 64 + 16 * j + r16, p.N - 1 - n0) * p.ldw, ke, p.K);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      fe.a[i] = fetch_end(a0 + (long long)min(wm * 64 + 16 * i + r16, p.M - 1 - m0) * p.lda, ke, p.K);
+  }
   // Stage s + 1 has landed everywhere, and everybody has read stage s, after the
   // barrier of step s; the copies of the two stages behind it may be under way.
   if constexpr (kDma) wait_dma<3 * kMidPieces>();
@@ -897,16 +916,12 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
     step(f0, f1, x0, s);
     if (s + 1 < steps) step(f1, f0, x1, s + 1);
   }
-  // the last bytes of the rows, straight from memory
-  if (grp == 1 && p.K > whole * kBK) {
-    const int k = whole * kBK + 16 * g;
+  if (ends) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      f0.w[j] = load_end(w0 + (long long)min(wn * 64 + 16 * j + r16, p.N - 1 - n0) * p.ldw, k, p.K);
+    for (int j = 0; j < 4; ++j) fe.w[j] = shift_end(fe.w[j], ke, p.K);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f0.a[i] = load_end(a0 + (long long)min(wm * 64 + 16 * i + r16, p.M - 1 - m0) * p.lda, k, p.K);
-    multiply(f0);
+    for (int i = 0; i < 4; ++i) fe.a[i] = shift_end(fe.a[i], ke, p.K);
+    multiply(fe);
   }
 
   wait_dma_all();                                     // no copy lands in what follows
