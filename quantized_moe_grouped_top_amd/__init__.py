@@ -143,30 +143,38 @@ def _current_functions():
     return _current
 
 
-def _enqueue(name, tensors, args, stream):
-    """Call `name` with `args` and `stream`, or the current stream of the device
-    that holds `tensors`, with that device current.  Tensors on the host or on
-    different devices are refused; integer addresses and None (an optional
-    argument left out) are taken as they are."""
-    f = getattr(_lib or lib(), name)
-    dev = None
+def _pointers(name, tensors):
+    """(device, device pointers) of the tensors of one call.  Tensors on the host
+    or on different devices are refused; integer addresses and None (an optional
+    argument left out) are taken as they are, and a call without tensors has
+    device None."""
+    dev, ptrs = None, []
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
+            ptrs.append(t)
             continue
         d = t.get_device()
         if d != dev:
             if dev is not None or d < 0:
                 raise MoeError(MOE_EINVAL, f"{name}: tensors must be on one GPU, got {t.device}")
             dev = d
-    if dev is None:
-        return _check(f(*args, _stream(stream)))
+        ptrs.append(t.data_ptr())
+    return dev, ptrs
+
+
+def _enqueue(f, dev, stream, *args):
+    """Call `f` with `args` and `stream`, or the current stream of device `dev`,
+    with that device current."""
     device, raw_stream = _current or _current_functions()
-    s = raw_stream(dev) if stream is None else _stream(stream)
-    if dev != device():
+    if dev is None:
+        rc = f(*args, _stream(stream))
+    elif dev == device():
+        rc = f(*args, raw_stream(dev) if stream is None else _stream(stream))
+    else:
         import torch
         with torch.cuda.device(dev):
-            return _check(f(*args, s))
-    return _check(f(*args, s))
+            rc = f(*args, raw_stream(dev) if stream is None else _stream(stream))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def _check(rc):
@@ -312,16 +320,16 @@ def moe_combine(y, M, N, top_k, out, stream=None):
 # ---- the layer around the grouped GEMMs ------------------------------------------
 def moe_route_topk(logits, dtype, ld, bias, M, E, top_k, score, n_group, topk_group, group_rule,
                    renormalize, scale, topk_ids, topk_weights, stream=None):
-    return _enqueue("moe_route_topk", (logits, bias, topk_ids, topk_weights),
-                    (_ptr(logits), dtype, ld, _ptr(bias), M, E, top_k, score, n_group, topk_group,
-                     group_rule, renormalize, scale, _ptr(topk_ids), _ptr(topk_weights)), stream)
+    dev, (x, b, i, w) = _pointers("moe_route_topk", (logits, bias, topk_ids, topk_weights))
+    return _enqueue((_lib or lib()).moe_route_topk, dev, stream, x, dtype, ld, b, M, E, top_k, score,
+                    n_group, topk_group, group_rule, renormalize, scale, i, w)
 
 
 def moe_route_topk_backward(d_weights, topk_ids, logits, dtype, ld, M, E, top_k, score,
                             renormalize, scale, d_logits, ldd, stream=None):
-    return _enqueue("moe_route_topk_backward", (d_weights, topk_ids, logits, d_logits),
-                    (_ptr(d_weights), _ptr(topk_ids), _ptr(logits), dtype, ld, M, E, top_k, score,
-                     renormalize, scale, _ptr(d_logits), ldd), stream)
+    dev, (g, i, x, d) = _pointers("moe_route_topk_backward", (d_weights, topk_ids, logits, d_logits))
+    return _enqueue((_lib or lib()).moe_route_topk_backward, dev, stream, g, i, x, dtype, ld, M, E,
+                    top_k, score, renormalize, scale, d, ldd)
 
 
 def moe_align_workspace_bytes(M, E, top_k):
@@ -330,12 +338,11 @@ def moe_align_workspace_bytes(M, E, top_k):
 
 def moe_align_topk_ids(topk_ids, M, E, top_k, block_m, expert_first, sorted_token_ids, expert_ids,
                        num_tokens_post_padded, expert_counts, workspace, stream=None):
-    return _enqueue("moe_align_topk_ids",
-                    (topk_ids, sorted_token_ids, expert_ids, num_tokens_post_padded,
-                     expert_counts, workspace),
-                    (_ptr(topk_ids), M, E, top_k, block_m, expert_first, _ptr(sorted_token_ids),
-                     _ptr(expert_ids), _ptr(num_tokens_post_padded), _ptr(expert_counts),
-                     _ptr(workspace)), stream)
+    dev, (i, s, e, n, c, ws) = _pointers(
+        "moe_align_topk_ids", (topk_ids, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                               expert_counts, workspace))
+    return _enqueue((_lib or lib()).moe_align_topk_ids, dev, stream, i, M, E, top_k, block_m,
+                    expert_first, s, e, n, c, ws)
 
 
 def moe_gemm_int8w8a8_workspace_bytes(M, K, N):
@@ -344,7 +351,7 @@ def moe_gemm_int8w8a8_workspace_bytes(M, K, N):
 
 def moe_gemm_int8w8a8(a_q, lda, a_scale, w_q, ldw, w_scale, bias, addend, M, K, N, out_dtype, out,
                       ldo, workspace, stream=None):
-    return _enqueue("moe_gemm_int8w8a8",
-                    (a_q, a_scale, w_q, w_scale, bias, addend, out, workspace),
-                    (_ptr(a_q), lda, _ptr(a_scale), _ptr(w_q), ldw, _ptr(w_scale), _ptr(bias),
-                     _ptr(addend), M, K, N, out_dtype, _ptr(out), ldo, _ptr(workspace)), stream)
+    dev, (a, sa, w, sw, b, c, o, ws) = _pointers(
+        "moe_gemm_int8w8a8", (a_q, a_scale, w_q, w_scale, bias, addend, out, workspace))
+    return _enqueue((_lib or lib()).moe_gemm_int8w8a8, dev, stream, a, lda, sa, w, ldw, sw, b, c, M, K,
+                    N, out_dtype, o, ldo, ws)
