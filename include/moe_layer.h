@@ -35,7 +35,7 @@ extern "C" {
                                          takes MOE_MAX_EXPERTS of them: see expert_first
                                          of moe_align_topk_ids) */
 #define MOE_MAX_ROUTE_GROUPS  64      /* n_group */
-#define MOE_MAX_ROUTE_TOKENS  (1 << 26)  /* M of the router lies below (one launch) */
+#define MOE_MAX_ROUTE_TOKENS  (1 << 25)  /* M of the router lies below (one launch) */
 #define MOE_MAX_INT8_K        131071  /* K of the int8 product: |sum| <= 128*128*K < 2^31 */
 
 /* ======================================================================== *

@@ -27,7 +27,7 @@ MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_SLOTS = 128, 8, 65536
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
-MOE_MAX_ROUTE_EXPERTS, MOE_MAX_ROUTE_GROUPS, MOE_MAX_ROUTE_TOKENS = 512, 64, 1 << 26
+MOE_MAX_ROUTE_EXPERTS, MOE_MAX_ROUTE_GROUPS, MOE_MAX_ROUTE_TOKENS = 512, 64, 1 << 25
 MOE_MAX_INT8_K = 131071
 
 EXPORTS = [

@@ -150,11 +150,16 @@ __device__ __forceinline__ double fma_const(double p, double r, double c) {
   asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(p), "v"(r), "s"(c));
   return d;
 }
-__device__ __forceinline__ double exp2_poly(double t) {
+// The leading coefficient, kept in vector registers by the caller.
+__device__ __forceinline__ double exp2_lead() {
+  double c = 1.0205905373362123e-07;
+  asm("" : "+v"(c));
+  return c;
+}
+__device__ __forceinline__ double exp2_poly(double t, double lead) {
   const double n = __builtin_rint(t);
   const double r = t - n;
-  double p = 1.0205905373362123e-07;
-  p = fma_const(p, r, 1.3259645246593194e-06);
+  double p = fma_const(lead, r, 1.3259645246593194e-06);
   p = fma_const(p, r, 1.525267292505434e-05);
   p = fma_const(p, r, 0.0001540343375123525);
   p = fma_const(p, r, 0.0013333558200794313);
@@ -170,9 +175,9 @@ constexpr double kLog2e = 1.4426950408889634;
 // 1 / (1 + exp(-x)) to about 2^-42 (absolute): beyond |x| = 80 the score is 0
 // or 1 within 2^-115, and 1 + exp(80) is still a float32, whose hardware
 // reciprocal starts one Newton step.
-__device__ __forceinline__ double sigmoid_key(float x) {
+__device__ __forceinline__ double sigmoid_key(float x, double lead) {
   const float c = __builtin_amdgcn_fmed3f(x, -80.0f, 80.0f);
-  const double d = 1.0 + exp2_poly(-kLog2e * (double)c);
+  const double d = 1.0 + exp2_poly(-kLog2e * (double)c, lead);
   const double y = (double)__builtin_amdgcn_rcpf((float)d);
   return fma(y, fma(-d, y, 1.0), y);
 }
@@ -180,8 +185,30 @@ __device__ __forceinline__ double sigmoid_key(float x) {
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // ---- router: sorted lists ------------------------------------------------------------
+// Larger and smaller of two keys (never NaN).  As instructions: the compiler's
+// fmax and fmin first quiet every operand that it knows nothing about, here one
+// in two.  It does not see either that these write registers which a lane
+// exchange may not read in the two cycles after: settle() goes in between.
+__device__ __forceinline__ double larger(double a, double b) {
+  double d;
+  asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+__device__ __forceinline__ double smaller(double a, double b) {
+  double d;
+  asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+__device__ __forceinline__ void settle(double (&a)[8]) {
+  asm volatile("s_nop 1"
+               : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(a[4]), "+v"(a[5]), "+v"(a[6]),
+                 "+v"(a[7]));
+}
+__device__ __forceinline__ void settle(double (&a)[2]) {
+  asm volatile("s_nop 1" : "+v"(a[0]), "+v"(a[1]));
+}
 __device__ __forceinline__ void exchange(double &a, double &b) {   // a >= b afterwards
-  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  const double hi = larger(a, b), lo = smaller(a, b);
   a = hi;
   b = lo;
 }
@@ -190,7 +217,7 @@ __device__ __forceinline__ void exchange(double &a, double &b) {   // a >= b aft
 template <int KK>
 __device__ __forceinline__ void merge_lists(double (&a)[KK], const double (&b)[KK]) {
 #pragma unroll
-  for (int i = 0; i < KK; ++i) a[i] = __builtin_fmax(a[i], b[KK - 1 - i]);
+  for (int i = 0; i < KK; ++i) a[i] = larger(a[i], b[KK - 1 - i]);
 #pragma unroll
   for (int d = KK / 2; d >= 1; d /= 2)
 #pragma unroll
@@ -201,6 +228,7 @@ template <int KK, int kStep, int kEnd>
 __device__ __forceinline__ void merge_lanes(double (&a)[KK]) {
   if constexpr (kStep < kEnd) {
     double b[KK];
+    settle(a);
 #pragma unroll
     for (int i = 0; i < KK; ++i) b[i] = lane_partner<kStep>(a[i]);
     merge_lists<KK>(a, b);
@@ -239,8 +267,8 @@ __device__ __forceinline__ void local_list(const double (&key)[V], double (&a)[K
     a[1] = -INFINITY;
 #pragma unroll
     for (int i = 1; i < V; ++i) {
-      a[1] = __builtin_fmax(a[1], __builtin_fmin(a[0], key[i]));
-      a[0] = __builtin_fmax(a[0], key[i]);
+      a[1] = larger(a[1], smaller(a[0], key[i]));
+      a[0] = larger(a[0], key[i]);
     }
   }
 }
@@ -250,9 +278,13 @@ template <int kStep, int kEnd>
 __device__ __forceinline__ void top2_lanes(double &m1, double &m2, int steps) {
   if constexpr (kStep < kEnd) {
     if (kStep < steps) {
+      double m[2] = {m1, m2};
+      settle(m);
+      m1 = m[0];
+      m2 = m[1];
       const double o1 = lane_partner<kStep>(m1), o2 = lane_partner<kStep>(m2);
-      m2 = __builtin_fmax(__builtin_fmin(m1, o1), __builtin_fmax(m2, o2));
-      m1 = __builtin_fmax(m1, o1);
+      m2 = larger(smaller(m1, o1), larger(m2, o2));
+      m1 = larger(m1, o1);
       top2_lanes<kStep + 1, kEnd>(m1, m2, steps);
     }
   }
@@ -305,6 +337,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
   float m = -INFINITY;
   double z = 0.0;
   double key[V], sc[V];
+  const double lead = exp2_lead();
   bool odd = false;                                        // NaN or infinities here
 #pragma unroll
   for (int u = 0; u < V; ++u) odd |= !(__builtin_fabsf(v[u]) < INFINITY);
@@ -317,7 +350,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       const double d = kLog2e * ((double)v[u] - (double)m);
-      sc[u] = d < -1100.0 ? 0.0 : exp2_poly(d);            // (a NaN stays one)
+      sc[u] = d < -1100.0 ? 0.0 : exp2_poly(d, lead);            // (a NaN stays one)
       if (e0 + u < E) z += sc[u];
     }
     z = lanes_sum<0, kSteps>(z);
@@ -326,7 +359,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     for (int u = 0; u < V; ++u) sc[u] *= inv;
   } else if (scored) {
 #pragma unroll
-    for (int u = 0; u < V; ++u) sc[u] = sigmoid_key(v[u]);
+    for (int u = 0; u < V; ++u) sc[u] = sigmoid_key(v[u], lead);
     if (__any(odd)) {
 #pragma unroll
       for (int u = 0; u < V; ++u) sc[u] = v[u] != v[u] ? (double)v[u] : sc[u];
@@ -362,8 +395,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     for (int u = 0; u < V; ++u) {
       const double w = top2 ? sc[u] : key[u];
       if (e0 + u < E) {
-        m2 = __builtin_fmax(m2, __builtin_fmin(m1, w));
-        m1 = __builtin_fmax(m1, w);
+        m2 = larger(m2, smaller(m1, w));
+        m1 = larger(m1, w);
       }
     }
     top2_lanes<0, kSteps>(m1, m2, lane_bits);
@@ -390,8 +423,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
       double m1 = s_key[tok][g * gs], m2 = -INFINITY;
       for (int q = 1; q < gs; ++q) {
         const double w = s_key[tok][g * gs + q];
-        m2 = __builtin_fmax(m2, __builtin_fmin(m1, w));
-        m1 = __builtin_fmax(m1, w);
+        m2 = larger(m2, smaller(m1, w));
+        m1 = larger(m1, w);
       }
       s_worth[tok][g] = group_worth(m1, m2, top2, g);
     }
@@ -450,11 +483,11 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
 }
 
 // ---- gradient -----------------------------------------------------------------
-// One token per G lanes.  Lane j takes the j-th choice and its share of the
-// sums; then every lane builds its V gradients by looking for its experts among
-// the choices (no two lanes write one expert, whatever the choices are).  The
-// plain softmax reads the whole row for its scores, the others only the chosen
-// logits.
+// One token per G lanes.  Lane j takes the j-th choice and its share of the sums
+// and puts its gradient into the token's row in LDS; then every lane stores the V
+// gradients of its experts.  A token with one expert twice is gathered choice by
+// choice instead, in their order.  The plain softmax reads the whole row for its
+// scores, the others only the chosen logits.
 template <int V>
 __device__ __forceinline__ void store_values(void *base, long long row_at, int dtype, bool vec,
                                              int e0, int E, const float (&v)[V]) {
@@ -501,10 +534,18 @@ __device__ __forceinline__ void store_values(void *base, long long row_at, int d
     if (e0 + u < E) x[u] = bf ? TypeBf16::store(v[u]) : TypeF16::store(v[u]);
 }
 
+// exp(x - m): the rounding of m log2(e) is the same for a whole row and leaves its
+// shares alone, the fused rest is as near as x - m.
+__device__ __forceinline__ float exp_less(float x, float m) {
+  constexpr float kL = 1.44269504f;
+  return __builtin_amdgcn_exp2f(fmaf(x, kL, -(m * kL)));
+}
+
 template <int G, int V, bool kDense>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs a, int dtype,
                                                              bool vec_in, bool vec_out) {
   constexpr int kTokens = 256 / G, kSteps = Log2<G>::value;
+  __shared__ __attribute__((aligned(16))) float s_row[kTokens][G * V];
   const int i = threadIdx.x & (G - 1), tok = threadIdx.x / G;
   const long long t = (long long)blockIdx.x * kTokens + tok;
   const bool live = t < a.M;
@@ -521,7 +562,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
     g = a.dw[row * k + i];
   }
   const bool valid = (unsigned)id < (unsigned)E;
-  if (!valid) id = -1;
+  if (!valid) {                                     // no choice: takes no part
+    id = -1;
+    g = 0.0f;
+  }
   if (valid) {
     if (dtype == MOE_F32) x = ((const float *)a.logits)[row * a.ld + id];
     else if (dtype == MOE_BF16) x = TypeBf16::load(((const uint16_t *)a.logits)[row * a.ld + id]);
@@ -538,14 +582,14 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
     float z = 0.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      p[u] = e0 + u < E ? expf(p[u] - m) : 0.0f;
+      p[u] = e0 + u < E ? exp_less(p[u], m) : 0.0f;
       z += p[u];
     }
     z = lanes_sum<0, kSteps>(z);
     const float inv = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
     for (int u = 0; u < V; ++u) p[u] *= inv;
-    const float pj = valid ? expf(x - m) * inv : 0.0f;
+    const float pj = valid ? exp_less(x, m) * inv : 0.0f;
     back = a.scale * lanes_sum<0, kSteps>(g * pj);
     d = a.scale * g;
   } else {
@@ -570,13 +614,30 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
 #pragma unroll
   for (int u = 0; u < V; ++u) o[u] = 0.0f;
   const int first = (threadIdx.x & 63) & ~(G - 1);
+  bool twice = false;                               // another choice has this expert
 #pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    if (j >= k) break;
-    const int at = __shfl(id, first + j) - e0;
-    const float dj = __shfl(d, first + j);
+  for (int j = 1; j < kMaxTopK; ++j)
+    twice |= __shfl(id, first + ((i + j) & (kMaxTopK - 1))) == id && valid && i < kMaxTopK;
+  if (__any(twice)) {
 #pragma unroll
-    for (int u = 0; u < V; ++u) o[u] += at == u ? dj : 0.0f;
+    for (int j = 0; j < kMaxTopK; ++j) {
+      if (j >= k) break;
+      const int at = __shfl(id, first + j) - e0;
+      const float dj = __shfl(d, first + j);
+#pragma unroll
+      for (int u = 0; u < V; ++u) o[u] += at == u ? dj : 0.0f;
+    }
+  } else {
+    // a wavefront's LDS accesses are carried out in order, and no other touches
+    // its tokens' rows
+    float *row_s = s_row[tok];
+#pragma unroll
+    for (int u = 0; u < V; ++u) row_s[e0 + u] = 0.0f;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (valid) row_s[id] = d;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < V; ++u) o[u] = row_s[e0 + u];
   }
   if constexpr (kDense) {
 #pragma unroll
@@ -592,7 +653,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
 // the slots' order.
 constexpr int kAlignThreads = 1024;
 constexpr int kAlignWaves = kAlignThreads / 64;
-constexpr int kOneWorkgroupChunks = 4;          // up to here one workgroup is as fast as many
+constexpr int kOneWorkgroupChunks = 2;          // up to here one workgroup is faster than two launches
 constexpr int kChunk = 1024;                     // slots of one workgroup where there are many
 
 // local expert of a slot, or -1
@@ -749,31 +810,41 @@ __global__ __launch_bounds__(kAlignThreads) void align_count_kernel(const AlignA
 // ... and, from the counts of all chunks, places its own.
 __global__ __launch_bounds__(kAlignThreads) void align_place_kernel(const AlignArgs a) {
   constexpr int kParts = kAlignThreads / kMaxExperts;
+  constexpr int kEach = kMaxSlots / kChunk / kParts;   // chunks of one thread at most
   __shared__ int s_wave[kAlignWaves][kMaxExperts];
   __shared__ int s_all[kParts][kMaxExperts], s_pre[kParts][kMaxExperts];
   __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts + 1];
-  const int tid = threadIdx.x, begin = blockIdx.x * kChunk, nbits = bits_for(a.E);
-  for (int x = tid; x < kAlignWaves * kMaxExperts; x += kAlignThreads) (&s_wave[0][0])[x] = 0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nbits = bits_for(a.E);
+  const int i = (int)blockIdx.x * kChunk + tid;        // this thread's slot
+  const int id = i < a.S ? a.ids[i] : 0;
   // slots of an expert in all chunks and in those before this one: every
-  // kParts-th chunk by one group of kMaxExperts threads
-  const int e = tid % kMaxExperts, part = tid / kMaxExperts, chunks = gridDim.x;
-  int all = 0, pre = 0;
-  if (e < a.E) {
-    for (int c = part; c < chunks; c += kParts) {
-      const int n = a.ws[c * a.E + e];
-      all += n;
-      pre += c < (int)blockIdx.x ? n : 0;
-    }
-  }
-  s_all[part][e] = all;
-  s_pre[part][e] = pre;
-  __syncthreads();
-  count_slots(a, begin, min(begin + kChunk, a.S), 64, nbits, s_wave);
-  if (tid < a.E) {
-    int n = 0;
+  // kParts-th chunk by one group of kMaxExperts threads, all loads at once
+  const int x = tid % kMaxExperts, part = tid / kMaxExperts, chunks = gridDim.x;
+  int n[kEach];
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) n += s_all[q][tid];
-    s_cnt[tid] = n;
+  for (int q = 0; q < kEach; ++q) {
+    const int c = part + q * kParts;
+    n[q] = x < a.E && c < chunks ? a.ws[c * a.E + x] : 0;
+  }
+  for (int q = tid; q < kAlignWaves * kMaxExperts; q += kAlignThreads) (&s_wave[0][0])[q] = 0;
+  const int e = i < a.S ? local_expert(id, a.expert_first, a.E) : -1;
+  const unsigned long long peers = peers_of(e, nbits);
+  const int rank = lanes_below(peers);
+  int all = 0, pre = 0;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    all += n[q];
+    pre += part + q * kParts < (int)blockIdx.x ? n[q] : 0;
+  }
+  s_all[part][x] = all;
+  s_pre[part][x] = pre;
+  __syncthreads();
+  if (e >= 0 && rank == 0) s_wave[wave][e] = __popcll(peers);
+  if (tid < kMaxExperts) {
+    int sum = 0;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) sum += s_all[q][tid];
+    s_cnt[tid] = sum;
   }
   __syncthreads();
   if (tid < 64) padded_starts(s_cnt, a.E, a.block_m, s_off);
@@ -784,13 +855,13 @@ __global__ __launch_bounds__(kAlignThreads) void align_place_kernel(const AlignA
     for (int q = 0; q < kParts; ++q) at += s_pre[q][tid];
 #pragma unroll
     for (int w = 0; w < kAlignWaves; ++w) {
-      const int n = s_wave[w][tid];
+      const int m = s_wave[w][tid];
       s_wave[w][tid] = at;
-      at += n;
+      at += m;
     }
   }
   __syncthreads();
-  place_slots(a, begin, min(begin + kChunk, a.S), 64, nbits, s_wave);
+  if (e >= 0) a.sorted_ids[s_wave[wave][e] + rank] = i;
   align_rest(a, s_off, s_cnt, blockIdx.x, chunks);
 }
 

@@ -349,6 +349,31 @@ def test_layer_with_general_router_and_shared_expert(M, E, k, fmt, block_m):
     assert np.all(np.abs(dx.double().cpu().numpy() - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -40)
 
 
+def test_layer_with_experts_on_two_devices():
+    """The experts in two windows, as two devices hold them: every slot's result
+    is the one of the layer that holds all, the other window leaves it zero, and
+    the sums add up."""
+    print("\n[layer] two windows", flush=True)
+    M, E, k, K, N = 50, 16, 4, 256, 128
+    g = _gen("windows")
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(M, E, generator=g).to(DEV)
+    w = (torch.randn(E, N, K, generator=g) / 16).to(DEV)
+    w_q, w_s = runner.quantize_weights(w, "int8dq")
+    whole = runner.RoutedMoE("int8dq", M, K, N, E, k, router=runner.TopKRouter(M, E, k, score="sigmoid"))
+    whole.forward(x, logits, w_q, w_s)
+    total = torch.zeros(M * k, N, device=DEV)
+    for first in (0, 8):
+        router = runner.TopKRouter(M, E, k, score="sigmoid", expert_first=first, n_local=8)
+        part = runner.RoutedMoE("int8dq", M, K, N, 8, k, router=router)
+        part.forward(x, logits, w_q[first:first + 8], w_s[first:first + 8])
+        torch.cuda.synchronize()
+        here = ((router.topk_ids >= first) & (router.topk_ids < first + 8)).view(-1)
+        assert torch.equal(part.y[here], whole.y[here]) and torch.all(part.y[~here] == 0)
+        total += part.y.view(torch.bfloat16).float()
+    assert torch.equal(total, whole.y.view(torch.bfloat16).float())
+
+
 def test_quantized_linear_chain():
     """Int8Linear quantizes bf16 rows per token (the codes and scales of the
     oracle) and multiplies."""

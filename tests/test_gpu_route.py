@@ -209,7 +209,7 @@ def _dense_tol(x, ids, g, scale):
     return scale * p * (up + total) * 2.0 ** -24 * (d + spread + 64)
 
 
-def check_backward(x, dtype, ids, g, score, renorm, scale, pad=0):
+def check_backward(x, dtype, ids, g, score, renorm, scale, pad=0, ref=None):
     M, E = x.shape
     k = ids.shape[1]
     full = torch.full((M + 1, E + pad), 77.0, dtype=DT[dtype][1], device=DEV)
@@ -218,7 +218,8 @@ def check_backward(x, dtype, ids, g, score, renorm, scale, pad=0):
     torch.cuda.synchronize()
     assert torch.all(full[M] == 77.0) and torch.all(full[:, E:] == 77.0)
     got = full[:M, :E].double().cpu().numpy()
-    xs, gs, cs = x.float().cpu().numpy(), g.cpu().numpy(), ids.cpu().numpy()
+    gs = (g if ref is None else ref).cpu().numpy()
+    xs, cs = x.float().cpu().numpy(), ids.cpu().numpy()
     ref = L.route_backward(gs, cs, xs, score, renorm, scale)
     eps = torch.finfo(DT[dtype][1]).eps / 2
     tiny = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -24}[dtype]
@@ -271,10 +272,12 @@ def test_route_backward_odd_choices_and_masks():
     x[7] = -300.0                                                  # sigmoid scores near 1e-131
     x[8] = 90.0
     x[9, ids[9].long()] = -inf                                     # all chosen masked
-    g = torch.randn(12, 4, generator=gen).to(DEV)
+    g = torch.randn(12, 4, generator=gen)
+    g[2, 2], g[3, 0], g[4, 0] = float("nan"), inf, float("nan")    # of choices that take no part
+    ref = torch.where(torch.isfinite(g), g, 0.0)
     for score in (0, 1):
         for renorm in (True, False):
-            check_backward(x, "f32", ids.to(DEV), g, score, renorm, 1.5, pad=1)
+            check_backward(x, "f32", ids.to(DEV), g.to(DEV), score, renorm, 1.5, pad=1, ref=ref)
 
 
 def test_route_backward_against_differences():

@@ -71,7 +71,7 @@ def _route(**kw):
     (dict(E=8, ld=8, top_k=2, n_group=8, topk_group=4), INV),     # two best of one expert
     (dict(logits=0), INV), (dict(topk_ids=None), INV), (dict(topk_weights=0), INV),
     (dict(logits=FAKE + 2), INV), (dict(bias=FAKE + 1), INV), (dict(topk_ids=FAKE + 2), INV),
-    (dict(dtype=1, logits=FAKE + 1), INV), (dict(M=1 << 26), UNS),
+    (dict(dtype=1, logits=FAKE + 1), INV), (dict(M=1 << 25), UNS),
 ])
 def test_route_rejects(kw, code):
     with pytest.raises(qm.MoeError) as ei:
