@@ -37,6 +37,8 @@ extern "C" {
 #define MOE_MAX_ROUTE_GROUPS  64      /* n_group */
 #define MOE_MAX_ROUTE_TOKENS  (1 << 25)  /* M of the router lies below (one launch) */
 #define MOE_MAX_INT8_K        131071  /* K of the int8 product: |sum| <= 128*128*K < 2^31 */
+#define MOE_MAX_INT8_ROWS     (1 << 27)  /* M of the int8 product lies below, M * N below
+                                         2^36 (one launch) */
 
 /* ======================================================================== *
  * Routing: scores, balance bias, groups, top-k, renormalised weights
@@ -59,8 +61,8 @@ extern "C" {
  *
  * Keys that rest on scores are computed in float64 and hold about 2^-40: of
  * two keys nearer than that either may come first (equal logits with equal
- * biases are exactly equal); what groups count is rounded to 38 bits.  Weights are computed in float64 and rounded
- * once to float32.
+ * biases are exactly equal); what groups count is rounded to 38 bits.  Weights
+ * are computed in float64 and rounded once to float32.
  * A logit or bias of -inf masks an expert: it is chosen only where fewer than
  * top_k others are left, and a -inf logit has score 0 (in a token without any
  * other logit every softmax score is 0).  A NaN key precedes every number, +inf
@@ -92,8 +94,8 @@ int moe_route_topk(const void *logits, int dtype, long long ld, const float *bia
  *                          dx_j = scale q_j (g_j - sum_i g_i q_i)
  *   plain softmax          dx_e = scale p_e (g_e [e chosen] - sum_i g_i p_i)
  * and 0 for every other expert: d_logits is written in full, in the type of
- * the logits.  The scores are computed again from the logits: in
- * float64 where only the chosen ones count, in float32 for the plain softmax.
+ * the logits.  The scores are computed again from the logits: in float64 where
+ * only the chosen ones count, in float32 for the plain softmax.
  * Ids outside [0, E) are no choice: they take no part.  An id that stands
  * twice in a token counts twice, in the sums and in its gradient.  A token
  * whose chosen scores are all 0 gets gradient 0.
@@ -101,7 +103,8 @@ int moe_route_topk(const void *logits, int dtype, long long ld, const float *bia
  *   d_weights [M, top_k] float32; topk_ids [M, top_k] int32
  *   logits    [M, E] of type dtype, rows ld elements apart
  *   d_logits  [M, E] of type dtype, rows ldd elements apart (ldd >= E);
- *             elements between the rows are not touched; may not overlap logits
+ *             elements between the rows are not touched; may be logits itself
+ *             (with ldd = ld), but not overlap it otherwise
  * E, top_k and M as for moe_route_topk. */
 int moe_route_topk_backward(const float *d_weights, const int *topk_ids, const void *logits,
                             int dtype, long long ld, int M, int E, int top_k, int score,
@@ -166,9 +169,10 @@ size_t moe_gemm_int8w8a8_workspace_bytes(int M, int K, int N);
  *   workspace moe_gemm_int8w8a8_workspace_bytes(M, K, N) bytes, 16-byte
  *           aligned, contents on entry ignored, one for each call that may run
  *           at the same time; or NULL (the same results, small shapes slower)
- * Any sizes: 1 <= K <= MOE_MAX_INT8_K, N >= 1, M >= 0; no alignment is required
- * beyond the types' own.  Fastest where a_q, w_q, lda and ldw are multiples of
- * 16 (K need not be). */
+ * Limits: 1 <= K <= MOE_MAX_INT8_K, 0 <= M < MOE_MAX_INT8_ROWS, N >= 1, rows less
+ * than 2^22 apart (so N < 2^22), M * N < 2^36; no alignment is required beyond
+ * the types' own.  Fastest where a_q, w_q, lda and ldw are multiples of 16 (K
+ * need not be). */
 int moe_gemm_int8w8a8(const int8_t *a_q, long long lda, const float *a_scale, const int8_t *w_q,
                       long long ldw, const float *w_scale, const float *bias, const void *addend,
                       int M, int K, int N, int out_dtype, void *out, long long ldo,

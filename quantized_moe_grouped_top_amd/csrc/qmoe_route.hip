@@ -534,11 +534,11 @@ __device__ __forceinline__ void store_values(void *base, long long row_at, int d
     if (e0 + u < E) x[u] = bf ? TypeBf16::store(v[u]) : TypeF16::store(v[u]);
 }
 
-// exp(x - m): the rounding of m log2(e) is the same for a whole row and leaves its
-// shares alone, the fused rest is as near as x - m.
+// exp(x - m).  The difference comes first: m log2(e) alone overflows where a whole
+// row holds its type's lowest value.
 __device__ __forceinline__ float exp_less(float x, float m) {
   constexpr float kL = 1.44269504f;
-  return __builtin_amdgcn_exp2f(fmaf(x, kL, -(m * kL)));
+  return __builtin_amdgcn_exp2f((x - m) * kL);
 }
 
 template <int G, int V, bool kDense>

@@ -280,6 +280,45 @@ def test_route_backward_odd_choices_and_masks():
             check_backward(x, "f32", ids.to(DEV), g.to(DEV), score, renorm, 1.5, pad=1, ref=ref)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_route_backward_of_the_largest_and_lowest_values(dtype):
+    """Rows masked with their type's lowest value, whole rows among them: all
+    logits are equal there, so every softmax score is 1 / E."""
+    print(f"\n[route backward] largest and lowest {dtype}", flush=True)
+    lowest = torch.finfo(DT[dtype][1]).min
+    for E, k in ((24, 4), (128, 8), (300, 5)):
+        gen = torch.Generator().manual_seed(E)
+        x = _logits(7, E, dtype, E).clone()
+        x[0] = lowest
+        x[1] = -lowest
+        x[2, ::2] = lowest
+        x[3] = lowest
+        x[3, 1] = -lowest                                          # one takes all
+        x[4, 3:] = -lowest                                         # E - 3 share
+        x[5, :] = lowest
+        x[5, 2] = 0.0
+        ids = torch.stack([torch.randperm(E, generator=gen)[:k] for _ in range(7)]).int().to(DEV)
+        g = torch.randn(7, k, generator=gen).to(DEV)
+        for score in (0, 1):
+            for renorm in (True, False):
+                check_backward(x, dtype, ids, g, score, renorm, 1.5)
+
+
+@pytest.mark.parametrize("score,renorm", [(0, False), (0, True), (1, False), (1, True)])
+def test_route_backward_in_place(score, renorm):
+    print("\n[route backward] in place", flush=True)
+    for M, E, dtype in ((1, 8, "f32"), (333, 60, "bf16"), (2000, 256, "f32"), (70, 512, "f16")):
+        gen = torch.Generator().manual_seed(E)
+        x = _logits(M, E, dtype, E + 1, pad=8)
+        ids = torch.stack([torch.randperm(E, generator=gen)[:8] for _ in range(M)]).int().to(DEV)
+        g = torch.randn(M, 8, generator=gen).to(DEV)
+        dx = torch.empty(M, E + 8, dtype=x.dtype, device=DEV)
+        for d in (dx, x):
+            qm.moe_route_topk_backward(g, ids, x, DT[dtype][0], E + 8, M, E, 8, score, renorm, 2.0, d, E + 8)
+        torch.cuda.synchronize()
+        assert torch.equal(dx[:, :E], x)
+
+
 def test_route_backward_against_differences():
     """The gradient of the kernel's own weights: sum_j g_j w_j by central
     differences.  The weights are float32 (half a step of 2^-24 of up to 1 on
