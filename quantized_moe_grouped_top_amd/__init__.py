@@ -28,7 +28,7 @@ MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_MAX_ROUTE_EXPERTS, MOE_MAX_ROUTE_GROUPS, MOE_MAX_ROUTE_TOKENS = 512, 64, 1 << 25
-MOE_MAX_INT8_K = 131071
+MOE_MAX_INT8_K, MOE_MAX_INT8_ROWS = 131071, 1 << 27
 
 EXPORTS = [
     "moe_last_error", "moe_last_hip_error", "moe_align_max_padded", "moe_recommended_block_m",

@@ -12,6 +12,10 @@ bool aligned_to(const void *p, int dtype) {
   return ((uintptr_t)p & (dtype == MOE_F32 ? 3u : 1u)) == 0;
 }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+// a launch holds fewer than 2^32 threads, up to 512 for 128 x 128 outputs
+bool int8_rows_fit(int M, int N) {
+  return M < MOE_MAX_INT8_ROWS && N < (1 << 22) && (long long)M * N < (1ll << 36);
+}
 
 // sizes shared by the router and its gradient
 int check_route(int dtype, long long ld, int M, int E, int top_k, int score, const char *fn) {
@@ -112,7 +116,7 @@ int moe_align_topk_ids(const int *topk_ids, int M, int E, int top_k, int block_m
 }
 
 size_t moe_gemm_int8w8a8_workspace_bytes(int M, int K, int N) {
-  if (M < 1 || N < 1 || K < 1 || K > MOE_MAX_INT8_K) return 0;
+  if (M < 1 || N < 1 || K < 1 || K > MOE_MAX_INT8_K || !int8_rows_fit(M, N)) return 0;
   return int8_workspace_bytes(M, K, N);
 }
 
@@ -125,6 +129,8 @@ int moe_gemm_int8w8a8(const int8_t *a_q, long long lda, const float *a_scale, co
   REQUIRE(M >= 0 && K >= 1 && N >= 1, MOE_EINVAL, "%s: M=%d K=%d N=%d", fn, M, K, N);
   REQUIRE(K <= MOE_MAX_INT8_K, MOE_EUNSUPPORTED, "%s: K=%d above %d (int32 sums)", fn, K,
           MOE_MAX_INT8_K);
+  REQUIRE(int8_rows_fit(M, N), MOE_EUNSUPPORTED, "%s: M=%d N=%d above %d, %d or 2^36 outputs", fn,
+          M, N, MOE_MAX_INT8_ROWS - 1, (1 << 22) - 1);
   REQUIRE(lda >= K && ldw >= K && ldo >= N, MOE_EINVAL,
           "%s: row distances %lld, %lld, %lld below K=%d, K, N=%d", fn, lda, ldw, ldo, K, N);
   // byte offsets inside a tile of 256 rows are 32-bit

@@ -94,6 +94,11 @@ def pack_weights(w_q, layout=MOE_W_TILED):
     return out
 
 
+def _rows_of(t, dtype, shape):
+    """t holds `shape` values of `dtype` without gaps."""
+    return t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()
+
+
 class TopKRouter:
     """General router of fixed (M, E, top_k): softmax or sigmoid scores, an
     optional balance bias, groups, renormalised weights.  `route` fills
@@ -120,6 +125,7 @@ class TopKRouter:
     def route(self, logits, bias=None):
         assert logits.dtype == self.torch_dtype and logits.shape == (self.M, self.E)
         assert logits.stride(1) == 1
+        assert bias is None or _rows_of(bias, torch.float32, (self.E,))
         moe_route_topk(logits, self.dtype, logits.stride(0), bias, self.M, self.E, self.top_k,
                        self.score, self.n_group, self.topk_group, self.group_rule,
                        self.renormalize, self.scale, self.topk_ids, self.topk_weights)
@@ -131,7 +137,9 @@ class TopKRouter:
 
     def backward(self, d_weights, logits):
         """d_logits [M, E] for d_weights [M, top_k], the choice held fixed."""
-        assert logits.dtype == self.torch_dtype and logits.stride(1) == 1
+        assert logits.dtype == self.torch_dtype and logits.shape == (self.M, self.E)
+        assert logits.stride(1) == 1
+        assert _rows_of(d_weights, torch.float32, (self.M, self.top_k))
         moe_route_topk_backward(d_weights, self.topk_ids, logits, self.dtype, logits.stride(0),
                                 self.M, self.E, self.top_k, self.score, self.renormalize,
                                 self.scale, self.d_logits, self.E)
@@ -145,11 +153,11 @@ class Int8Linear:
 
     def __init__(self, M, K, N, out="bf16", device="cuda"):
         self.M, self.K, self.N = M, K, N
-        self.dtype, torch_dtype = _DTYPES[out]
+        self.dtype, self.torch_dtype = _DTYPES[out]
         self.a_q = _empty((M, K), torch.int8, device)
         self.a_scale = _empty((max(M, 1),), torch.float32, device)
         self.ws = _empty((moe_gemm_int8w8a8_workspace_bytes(M, K, N),), torch.uint8, device)
-        self.out = _empty((M, N), torch_dtype, device)
+        self.out = _empty((M, N), self.torch_dtype, device)
 
     def quantize(self, x):
         moe_quantize_act(x, self.M, self.K, MOE_Q_INT8_PER_CHANNEL, None, 1, self.a_q,
@@ -157,6 +165,14 @@ class Int8Linear:
 
     def gemm(self, w_q, w_scale, bias=None, addend=None, out=None):
         out = self.out if out is None else out
+        assert w_q.dtype == torch.int8 and w_q.shape == (self.N, self.K) and w_q.stride(1) == 1
+        assert w_scale.dtype == torch.float32 and w_scale.numel() == self.N and w_scale.is_contiguous()
+        assert bias is None or _rows_of(bias, torch.float32, (self.N,))
+        # the bits of 16-bit values may come as int16
+        for t in (out, addend):
+            assert t is None or (tuple(t.shape) == (self.M, self.N) and t.is_contiguous() and
+                                 (t.dtype == self.torch_dtype or
+                                  (t.dtype == torch.int16 and self.dtype == MOE_BF16)))
         moe_gemm_int8w8a8(self.a_q, self.K, self.a_scale, w_q, w_q.stride(0), w_scale, bias, addend,
                           self.M, self.K, self.N, self.dtype, out, self.N, self.ws)
         return out

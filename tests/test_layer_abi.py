@@ -151,6 +151,43 @@ def test_int8_rejects(kw, code):
 
 @needs_lib
 @no_gpu
+@pytest.mark.parametrize("kw", [
+    dict(M=1 << 27), dict(M=2147483647), dict(N=1 << 22, ldo=1 << 22),
+    dict(M=1 << 26, N=1 << 10, ldo=1 << 10), dict(M=(1 << 27) - 1, N=513, ldo=513)])
+def test_int8_rejects_more_than_one_launch_holds(kw):
+    with pytest.raises(qm.MoeError) as ei:
+        _int8(**kw)
+    assert ei.value.code == UNS
+    sizes = dict(M=16, K=64, N=32)
+    sizes.update({k: v for k, v in kw.items() if k in sizes})
+    assert qm.moe_gemm_int8w8a8_workspace_bytes(**sizes) == 0
+
+
+@needs_lib
+@no_gpu
+def test_runner_classes_refuse_other_shapes_and_types():
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    r = runner.TopKRouter(4, 8, 2, device="cpu")
+    x, g = torch.zeros(4, 8), torch.zeros(4, 2)
+    for call in (lambda: r.route(x.double()), lambda: r.route(x[:3]), lambda: r.route(x.t()),
+                 lambda: r.route(x, torch.zeros(7)), lambda: r.route(x, torch.zeros(8).double()),
+                 lambda: r.backward(torch.zeros(2, 4).t(), x), lambda: r.backward(g.double(), x),
+                 lambda: r.backward(g, x[:3])):
+        with pytest.raises(AssertionError):
+            call()
+    lin = runner.Int8Linear(4, 32, 16, device="cpu")
+    w, s = torch.zeros(16, 32, dtype=torch.int8), torch.zeros(16)
+    out = torch.zeros(4, 16, dtype=torch.bfloat16)
+    for call in (lambda: lin.gemm(w.t(), s), lambda: lin.gemm(w[:8], s), lambda: lin.gemm(w, s[:8]),
+                 lambda: lin.gemm(w, s, bias=torch.zeros(8)), lambda: lin.gemm(w, s, out=out.float()),
+                 lambda: lin.gemm(w, s, addend=out[:, :8]), lambda: lin.gemm(w, s, addend=out[:2])):
+        with pytest.raises(AssertionError):
+            call()
+
+
+@needs_lib
+@no_gpu
 def test_no_tokens_is_valid():
     assert _route(M=0, logits=None, topk_ids=None, topk_weights=None) == qm.MOE_OK
     assert _bwd(M=0, logits=None, d_logits=None) == qm.MOE_OK
