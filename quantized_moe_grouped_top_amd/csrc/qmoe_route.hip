@@ -257,7 +257,7 @@ __device__ __forceinline__ void local_list(const double (&key)[V], double (&a)[K
     for (int q = 8; q < V; q += 8) {
       double b[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = key[q + i];
+      for (int i = 0; i < 8; ++i) b[i] = q + i < V ? key[q + i < V ? q + i : 0] : -INFINITY;
       sort8(b);
       merge_lists<8>(a, b);
     }
@@ -421,6 +421,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     __syncthreads();
     for (int g = i; g < a.n_group; g += G) {
       double m1 = s_key[tok][g * gs], m2 = -INFINITY;
+#pragma unroll 8
       for (int q = 1; q < gs; ++q) {
         const double w = s_key[tok][g * gs + q];
         m2 = larger(m2, smaller(m1, w));
@@ -432,6 +433,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     for (int g = i; g < a.n_group; g += G) {
       const double w = s_worth[tok][g];
       int before = 0;
+#pragma unroll 8
       for (int o = 0; o < a.n_group; ++o) before += s_worth[tok][o] > w;
       s_keep[tok][g] = before < a.topk_group;
     }
@@ -875,6 +877,12 @@ bool vector_rows(const void *p, long long ld, int dtype, int E, int V) {
   return ((uintptr_t)p & 15u) == 0 && bytes % 16 == 0 && E % V == 0;
 }
 
+// Groups of gs experts are 2^n whole lanes of V.
+bool whole_lanes(int gs, int V) {
+  const int lanes = gs / V;
+  return gs % V == 0 && (lanes & (lanes - 1)) == 0;
+}
+
 template <int G, int V>
 hipError_t route_with(const RouteArgs &a, int dtype, hipStream_t s) {
   const bool vec = vector_rows(a.logits, a.ld, dtype, a.E, V);
@@ -882,7 +890,7 @@ hipError_t route_with(const RouteArgs &a, int dtype, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(256);
   const int gs = a.E / a.n_group, lanes = gs / V;
   const bool grouped = a.topk_group < a.n_group;
-  const bool by_lanes = gs % V == 0 && (lanes & (lanes - 1)) == 0;
+  const bool by_lanes = whole_lanes(gs, V);
   int bits = 0;
   while ((1 << bits) < lanes) ++bits;
 #define QMOE_ROUTE(kk, mode) \
@@ -917,22 +925,35 @@ hipError_t backward_with(const RouteBwdArgs &a, int dtype, hipStream_t s) {
 // Lanes and keys per lane.  Few tokens: four keys, the shortest way through the
 // lane's sort (64 tokens of 256 experts 4.9 us, with eight keys 5.8).  From a
 // wavefront on every SIMD on, eight: fewer lanes repeat the merges (16384 tokens
-// of 128 experts: 5.5 us, with four 8.3).  From 8192 tokens on sixteen (16384
-// tokens of 256 experts in groups: 15.0 us, with eight 16.7, with four 24.2;
-// 4096 of 128: 5.1 with eight and sixteen).
+// of 128 experts: 5.5 us, with four 8.3).  From 8192 tokens on 16 to 24, by which
+// the lanes have work best (16384 tokens with 16 keys and with the number taken:
+// 160 experts 9.9, 7.5 us, 320 17.9, 12.4; of 256 in groups 14.9, with eight
+// 16.7).  Groups that are no whole lanes go through LDS, which costs more
+// than the wider lanes save: those stay at eight keys (16384 tokens of 200 experts
+// in 8 groups 18.5 us, with sixteen 23.7; 256 in 32 groups, whole lanes of eight,
+// 17.6, with sixteen 25.3; 160 in 8, whole lanes of twenty, 9.2, with sixteen 20.4).
 hipError_t launch_route_topk(const RouteArgs &a, int dtype, hipStream_t s) {
   constexpr int kWaves = 1024;                       // SIMDs of the card
   if (a.E <= 8) return route_with<8, 1>(a, dtype, s);
   if (a.E <= 32) return route_with<8, 4>(a, dtype, s);
   if (a.E <= 64) return route_with<8, 8>(a, dtype, s);
-  const bool few = (long long)a.M * (a.E <= 128 ? 32 : 64) <= 64 * kWaves, many = a.M >= 8192;
-  if (a.E <= 128)
-    return few ? route_with<32, 4>(a, dtype, s)
-               : many ? route_with<8, 16>(a, dtype, s) : route_with<16, 8>(a, dtype, s);
-  if (a.E <= 256)
-    return few ? route_with<64, 4>(a, dtype, s)
-               : many ? route_with<16, 16>(a, dtype, s) : route_with<32, 8>(a, dtype, s);
-  return many ? route_with<32, 16>(a, dtype, s) : route_with<64, 8>(a, dtype, s);
+  const bool few = (long long)a.M * (a.E <= 128 ? 32 : 64) <= 64 * kWaves;
+  const bool grouped = a.topk_group < a.n_group;
+#define QMOE_MANY(limit, G, V) \
+  if (a.E <= limit && (!grouped || whole_lanes(a.E / a.n_group, V))) return route_with<G, V>(a, dtype, s);
+  if (a.M >= 8192) {
+    QMOE_MANY(128, 8, 16)
+    QMOE_MANY(160, 8, 20)
+    QMOE_MANY(192, 8, 24)
+    QMOE_MANY(256, 16, 16)
+    QMOE_MANY(320, 16, 20)
+    QMOE_MANY(384, 16, 24)
+    QMOE_MANY(512, 32, 16)
+  }
+#undef QMOE_MANY
+  if (a.E <= 128) return few ? route_with<32, 4>(a, dtype, s) : route_with<16, 8>(a, dtype, s);
+  if (a.E <= 256) return few ? route_with<64, 4>(a, dtype, s) : route_with<32, 8>(a, dtype, s);
+  return route_with<64, 8>(a, dtype, s);
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, int dtype, hipStream_t s) {

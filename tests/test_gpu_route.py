@@ -186,6 +186,29 @@ def test_route_many_tokens(M, E, n, keep):
             assert np.all(np.abs(w[rows] - w0) <= 2.0 ** -23 * w0)
 
 
+@pytest.mark.parametrize("E,n,keep", [(160, 8, 3), (150, 5, 2), (192, 8, 4), (176, 2, 1), (200, 8, 3),
+                                      (256, 32, 8), (320, 16, 4), (300, 5, 2), (384, 8, 3), (370, 37, 9),
+                                      (130, 10, 3)])
+def test_route_many_tokens_of_odd_numbers_of_experts(E, n, keep):
+    """20 and 24 keys a lane, groups of whole lanes and others."""
+    M = 8200
+    print(f"\n[route] many M={M} E={E}", flush=True)
+    for dtype, pad in (("f32", 0), ("bf16", 0), ("f16", 3)):
+        x = _logits(M, E, dtype, _seed(M, E, dtype), pad=pad)
+        x[M - 3, 1::2] = float("-inf")
+        b = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(3))).to(DEV)
+        rows = np.r_[0:20, M // 2:M // 2 + 20, M - 20:M]
+        xs = x.float().cpu().numpy()[rows]
+        for k in (2, 8):
+            for bias, score, groups, rule, renorm in ((b, 1, n, 1, True), (None, 0, 1, 0, False),
+                                                      (b, 0, n, 0, False), (None, 1, n, 1, True)):
+                ids, w = route(x, dtype, k, bias, score, groups, keep if groups > 1 else 1, rule, renorm, 2.5)
+                ids0, w0 = L.route_general(xs, None if bias is None else b.cpu().numpy(), k, score, groups,
+                                           keep if groups > 1 else 1, rule, renorm, 2.5)
+                assert np.array_equal(ids[rows], ids0)
+                assert np.all(np.abs(w[rows] - w0) <= 2.0 ** -23 * w0)
+
+
 # ---- gradient ----------------------------------------------------------------------
 def _dense_tol(x, ids, g, scale):
     """Bound for the dense softmax gradient in float32.  p = exp(x - m) / Z:
