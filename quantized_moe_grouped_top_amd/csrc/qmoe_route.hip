@@ -10,9 +10,38 @@ namespace {
 // G neighbouring lanes share a token; lane i of them holds the experts i*V ..
 // i*V + V - 1 in registers.
 
+// A lane's vectors of a row of whole vectors, `left` elements from its end on: all
+// at once where the row has them all (a few percent faster than one by one).
+template <typename T, typename Vec, int n>
+__device__ __forceinline__ void load_vectors(const T *x, int left, Vec (&q)[n]) {
+  constexpr int kEach = sizeof(Vec) / sizeof(T);
+  if (left >= n * kEach) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) q[i] = *reinterpret_cast<const Vec *>(x + i * kEach);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      q[i] = Vec{};
+      if (left > i * kEach) q[i] = *reinterpret_cast<const Vec *>(x + i * kEach);
+    }
+  }
+}
+template <typename T, typename Vec, int n>
+__device__ __forceinline__ void store_vectors(T *x, int left, const Vec (&q)[n]) {
+  constexpr int kEach = sizeof(Vec) / sizeof(T);
+  if (left >= n * kEach) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) *reinterpret_cast<Vec *>(x + i * kEach) = q[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      if (left > i * kEach) *reinterpret_cast<Vec *>(x + i * kEach) = q[i];
+  }
+}
+
 // V values of a row from element e0 on as float32; elements at or past E read 0.
-// `vec`: rows and base are 16-byte aligned and V divides E, so a lane's values
-// exist all or not at all and load as whole words.
+// `vec`: rows and base are 16-byte aligned and E is whole vectors (vector_rows), so
+// a vector's values exist all or not at all.
 template <int V>
 __device__ __forceinline__ void load_values(const void *base, long long row_at, int dtype, bool vec,
                                             int e0, int E, float (&v)[V]) {
@@ -22,14 +51,10 @@ __device__ __forceinline__ void load_values(const void *base, long long row_at, 
     const float *x = (const float *)base + row_at + e0;
     if constexpr (V % 4 == 0) {
       if (vec) {
-        if (e0 < E) {
+        f32x4 q[V / 4];
+        load_vectors(x, E - e0, q);
 #pragma unroll
-          for (int u = 0; u < V; u += 4) {
-            const f32x4 q = *reinterpret_cast<const f32x4 *>(x + u);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[u + c] = q[c];
-          }
-        }
+        for (int u = 0; u < V; ++u) v[u] = q[u / 4][u % 4];
         return;
       }
     }
@@ -42,18 +67,15 @@ __device__ __forceinline__ void load_values(const void *base, long long row_at, 
   const bool bf = dtype == MOE_BF16;
   if constexpr (V % 4 == 0) {
     if (vec) {
-      if (e0 < E) {
-        constexpr int kW = V % 8 == 0 ? 4 : 2;             // dwords per load
-        typedef uint32_t words __attribute__((ext_vector_type(kW)));
+      constexpr int kW = V % 8 == 0 ? 4 : 2;               // dwords per load
+      typedef uint32_t words __attribute__((ext_vector_type(kW)));
+      words q[V / (2 * kW)];
+      load_vectors(x, E - e0, q);
 #pragma unroll
-        for (int u = 0; u < V; u += 2 * kW) {
-          const words q = *reinterpret_cast<const words *>(x + u);
-#pragma unroll
-          for (int c = 0; c < kW; ++c) {
-            v[u + 2 * c] = bf ? bf16_bits_to_f32(q[c] & 0xFFFFu) : TypeF16::load((uint16_t)q[c]);
-            v[u + 2 * c + 1] = bf ? bf16_bits_to_f32(q[c] >> 16) : TypeF16::load((uint16_t)(q[c] >> 16));
-          }
-        }
+      for (int u = 0; u < V; u += 2) {
+        const uint32_t two = q[u / (2 * kW)][u / 2 % kW];
+        v[u] = bf ? bf16_bits_to_f32(two & 0xFFFFu) : TypeF16::load((uint16_t)two);
+        v[u + 1] = bf ? bf16_bits_to_f32(two >> 16) : TypeF16::load((uint16_t)(two >> 16));
       }
       return;
     }
@@ -497,11 +519,10 @@ __device__ __forceinline__ void store_values(void *base, long long row_at, int d
     float *x = (float *)base + row_at + e0;
     if constexpr (V % 4 == 0) {
       if (vec) {
-        if (e0 < E) {
+        f32x4 q[V / 4];
 #pragma unroll
-          for (int u = 0; u < V; u += 4)
-            *reinterpret_cast<f32x4 *>(x + u) = f32x4{v[u], v[u + 1], v[u + 2], v[u + 3]};
-        }
+        for (int u = 0; u < V; ++u) q[u / 4][u % 4] = v[u];
+        store_vectors(x, E - e0, q);
         return;
       }
     }
@@ -514,20 +535,15 @@ __device__ __forceinline__ void store_values(void *base, long long row_at, int d
   const bool bf = dtype == MOE_BF16;
   if constexpr (V % 4 == 0) {
     if (vec) {
-      if (e0 < E) {
-        constexpr int kW = V % 8 == 0 ? 4 : 2;
-        typedef uint32_t words __attribute__((ext_vector_type(kW)));
+      constexpr int kW = V % 8 == 0 ? 4 : 2;
+      typedef uint32_t words __attribute__((ext_vector_type(kW)));
+      words q[V / (2 * kW)];
 #pragma unroll
-        for (int u = 0; u < V; u += 2 * kW) {
-          words q;
-#pragma unroll
-          for (int c = 0; c < kW; ++c)
-            q[c] = bf ? f32x2_to_bf16x2(v[u + 2 * c], v[u + 2 * c + 1])
-                      : (uint32_t)TypeF16::store(v[u + 2 * c]) |
-                            ((uint32_t)TypeF16::store(v[u + 2 * c + 1]) << 16);
-          *reinterpret_cast<words *>(x + u) = q;
-        }
-      }
+      for (int u = 0; u < V; u += 2)
+        q[u / (2 * kW)][u / 2 % kW] =
+            bf ? f32x2_to_bf16x2(v[u], v[u + 1])
+               : (uint32_t)TypeF16::store(v[u]) | ((uint32_t)TypeF16::store(v[u + 1]) << 16);
+      store_vectors(x, E - e0, q);
       return;
     }
   }
@@ -655,7 +671,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
 // the slots' order.
 constexpr int kAlignThreads = 1024;
 constexpr int kAlignWaves = kAlignThreads / 64;
-constexpr int kOneWorkgroupChunks = 2;          // up to here one workgroup is faster than two launches
+// Chunks up to which one workgroup does it all: 2048 slots 4.4 - 6.2 us by the
+// number of experts, two launches 6.5; 2560 of 128 experts 7.7 against 6.5.
+constexpr int kOneWorkgroupChunks = 2;
 constexpr int kChunk = 1024;                     // slots of one workgroup where there are many
 
 // local expert of a slot, or -1
@@ -871,10 +889,11 @@ __global__ __launch_bounds__(kAlignThreads) void align_place_kernel(const AlignA
 
 namespace {
 
-// Rows and base 16-byte aligned, and whole lanes of V values.
+// Rows and base 16-byte aligned, and whole vectors in a row: 16 bytes, of the 16-bit
+// types 8 where a lane's V values are no multiple of 16 bytes.
 bool vector_rows(const void *p, long long ld, int dtype, int E, int V) {
   const long long bytes = ld * (dtype == MOE_F32 ? 4 : 2);
-  return ((uintptr_t)p & 15u) == 0 && bytes % 16 == 0 && E % V == 0;
+  return ((uintptr_t)p & 15u) == 0 && bytes % 16 == 0 && E % (dtype == MOE_F32 || V % 8 ? 4 : 8) == 0;
 }
 
 // Groups of gs experts are 2^n whole lanes of V.
