@@ -328,8 +328,8 @@ enum { kNoGroups = 0, kLaneGroups = 1, kAnyGroups = 2 };
 // One token per G lanes.  The scores that keys rest on are computed in float64
 // by a polynomial; every lane sorts its V keys, and log2(G) merges of sorted
 // lists of KK leave the token's choice in every lane.  Groups: kLaneGroups
-// where a group is 2^n whole lanes, joined by lane steps; kAnyGroups ranks them
-// through LDS.
+// where a group is 2^n whole lanes (n = lane_bits), joined by lane steps;
+// kAnyGroups ranks them through LDS, 2^lane_bits lanes a group.
 template <int G, int V, int KK, int kGroups>
 __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int dtype, bool vec,
                                                          int lane_bits) {
@@ -441,15 +441,21 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
 #pragma unroll
     for (int u = 0; u < V; ++u) s_key[tok][e0 + u] = top2 ? sc[u] : key[u];
     __syncthreads();
-    for (int g = i; g < a.n_group; g += G) {
-      double m1 = s_key[tok][g * gs], m2 = -INFINITY;
-#pragma unroll 8
-      for (int q = 1; q < gs; ++q) {
-        const double w = s_key[tok][g * gs + q];
-        m2 = larger(m2, smaller(m1, w));
-        m1 = larger(m1, w);
+    // 2^lane_bits lanes scan a group
+    const int each = 1 << lane_bits, part = i & (each - 1);
+    for (int g0 = 0; g0 < a.n_group; g0 += G >> lane_bits) {
+      const int g = g0 + (i >> lane_bits);
+      double m1 = -INFINITY, m2 = -INFINITY;
+      if (g < a.n_group) {
+#pragma unroll 4
+        for (int q = part; q < gs; q += each) {
+          const double w = s_key[tok][g * gs + q];
+          m2 = larger(m2, smaller(m1, w));
+          m1 = larger(m1, w);
+        }
       }
-      s_worth[tok][g] = group_worth(m1, m2, top2, g);
+      top2_lanes<0, kSteps>(m1, m2, lane_bits);
+      if (g < a.n_group && part == 0) s_worth[tok][g] = group_worth(m1, m2, top2, g);
     }
     __syncthreads();
     for (int g = i; g < a.n_group; g += G) {
@@ -910,8 +916,9 @@ hipError_t route_with(const RouteArgs &a, int dtype, hipStream_t s) {
   const int gs = a.E / a.n_group, lanes = gs / V;
   const bool grouped = a.topk_group < a.n_group;
   const bool by_lanes = whole_lanes(gs, V);
+  // lanes of a group: those that hold it, or as many as there are for its scan
   int bits = 0;
-  while ((1 << bits) < lanes) ++bits;
+  while (by_lanes ? (1 << bits) < lanes : (a.n_group << (bits + 1)) <= G) ++bits;
 #define QMOE_ROUTE(kk, mode) \
   hipLaunchKernelGGL((route_topk_kernel<G, V, kk, mode>), grid, block, 0, s, a, dtype, vec, bits)
 #define QMOE_ROUTE_K(mode)                 \
