@@ -745,12 +745,15 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args p, int sp
 // multiplied; one barrier a stage.  The groups' exact sums meet in LDS.  Without
 // kDma (rows that begin at any byte) a stage passes through registers: fetched
 // two steps before it is written to LDS, which is one before it is read.
+// With `splits` > 1, workgroup (tile, y) contracts the y-th share of k and leaves
+// its sums in p.ws for int8_join_kernel.
 constexpr int kMM = 128, kMN = 128;
 constexpr int kMidSlot = (kMM + kMN) * kBK;          // 16 KB
 constexpr int kMidPieces = 4;
 
 template <typename Ty, bool kDma>
-__global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, TileOrder order) {
+__global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, TileOrder order,
+                                                           int splits) {
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kRing * kMidSlot];
   __shared__ float s_sa[kMM], s_sw[kMN], s_bias[kMN];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -765,8 +768,11 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
   const int m0 = tm * kMM, n0 = tn * kMN;
   const int8_t *a0 = p.a + (long long)m0 * p.lda, *w0 = p.w + (long long)n0 * p.ldw;
 
-  const int whole = p.K / kBK;                        // whole stages: group 0 the first half
-  const int first = grp ? (whole + 1) / 2 : 0;
+  // this share's whole stages: group 0 the first half
+  const int all = p.K / kBK, y = blockIdx.y;
+  const int from = (int)((long long)all * y / splits);
+  const int whole = (int)((long long)all * (y + 1) / splits) - from;
+  const int first = from + (grp ? (whole + 1) / 2 : 0);
   const int mine = grp ? whole / 2 : (whole + 1) / 2, steps = (whole + 1) / 2;
 
   // this wavefront's copies: rows 32 w .. of both operands, w its number in the group
@@ -866,8 +872,8 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
   }
   // the last bytes of the rows, straight from memory: fetched here, used at the end
   Frags fe;
-  const bool ends = grp == 1 && p.K > whole * kBK;
-  const int ke = whole * kBK + 16 * g;
+  const bool ends = grp == 1 && y == splits - 1 && p.K > all * kBK;
+  const int ke = all * kBK + 16 * g;
   if (ends) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -944,6 +950,16 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       sum[j] = (grp ? acc[i + 2][j] : acc[i][j]) + part[((other * 2 + i) * 4 + j) * 64 + lane];
+    if (splits > 1) {
+      const int m = m0 + ml, np = padded_cols(p.N);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + wn * 64 + 16 * j + 4 * g;
+        if (m < p.M && n < np)
+          *reinterpret_cast<i32x4 *>(p.ws + ((long long)y * p.M + m) * np + n) = sum[j];
+      }
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 4; j += 2)
       store_run<Ty>(p, m0 + ml, n0, wn * 64 + 16 * j, g, sa, s_sw, s_bias, sum[j], sum[j + 1]);
@@ -995,7 +1011,12 @@ StagedShape staged_shape(int M, int K, int N) {
   StagedShape best{mb, 1, 1, 1e300};
   for (int i = 0; i < (mb == 1 ? 2 : 3); ++i) {
     const long long tiles = tiles_of(M, N, 16 * mb, 16 << i);
-    const double us = mb == 1 ? kFew[i].of(tiles, 2 * kCus, K) : kMore[i].of(tiles, kCus, K);
+    double us = mb == 1 ? kFew[i].of(tiles, 2 * kCus, K) : kMore[i].of(tiles, kCus, K);
+    // every tile reads its rows of both operands, at 14 TB/s together (by that count
+    // 128 x 128 tiles in shares: 512 x 14336 x 4096 76.0 -> 47.7 us, 256 x 14336 x
+    // 4096 39.6 -> 30.8; nearest border 256 x 14336 x 2048 21.9, in shares 24.2)
+    const double read = (double)tiles * (16 * mb + (16 << i)) * K / 14e6;
+    if (mb > 1 && us < read) us = read;
     if (us < best.us) best = {mb, 1 << i, 1, us};
   }
   // Shares of k where the tiles leave three quarters of the CUs idle and each
@@ -1010,18 +1031,47 @@ StagedShape staged_shape(int M, int K, int N) {
   return best;
 }
 
+// 128 x 128 tiles, in shares of k where the tiles are few and the sums' way through
+// the workspace costs less than it saves: 4.5 us for the second launch and 4 TB/s
+// for the sums (whole, in shares: 512 x 14336 x 4096 60.3, 47.1 us, 384 x 14336 x
+// 4096 58.8, 42.0, 768 x 8192 x 2048 34.3, 29.5).  All shares run at once: each XCD
+// has 32 CUs for its run of the tiles (84 tiles in three shares, 33 a XCD: 35.2 us,
+// in two 25.3).
+struct MidShape {
+  int splits;
+  double us;
+};
+MidShape mid_shape(int M, int K, int N) {
+  constexpr Cost kMidCost{2.7, 18.0};
+  const long long tiles = tiles_of(M, N, kMM, kMN), run = (tiles + kXcds - 1) / kXcds;
+  MidShape best{1, kMidCost.of(tiles, kCus, K)};
+  for (int s = 2; s <= 16 && run * s <= kCus / kXcds && K / kBK >= 8 * s; ++s) {
+    const double us = 2.7 + 18.0 * K / 4096.0 / s + 4.5 + 8.0 * s * M * (double)N / 4e6;
+    if (us < best.us) best = {s, us};
+  }
+  return best;
+}
+
 enum Kind { kStaged, kMid, kBig };
 Kind kind_of(int M, int K, int N) {
-  constexpr Cost kMidCost{2.7, 18.0}, kBigCost{5.5, 33.0};
+  constexpr Cost kBigCost{5.5, 33.0};
   const double staged = staged_shape(M, K, N).us;
-  const double mid = kMidCost.of(tiles_of(M, N, kMM, kMN), kCus, K);
+  const double mid = mid_shape(M, K, N).us;
   const double big = kBigCost.of(tiles_of(M, N, kBM, kBN), kCus, K);
   if (staged <= mid && staged <= big) return kStaged;
   return mid < big ? kMid : kBig;
 }
 
-size_t staged_bytes(const StagedShape &t, int M, int N) {
-  return t.splits == 1 ? 0 : (size_t)t.splits * M * ((N + 3) / 4 * 4) * sizeof(int);
+size_t sums_bytes(int splits, int M, int N) {
+  return splits == 1 ? 0 : (size_t)splits * M * ((N + 3) / 4 * 4) * sizeof(int);
+}
+
+template <typename Ty>
+hipError_t launch_join(const Int8Args &a, int splits, hipStream_t s) {
+  const long long quads = (long long)a.M * ((a.N + 3) / 4);
+  hipLaunchKernelGGL(int8_join_kernel<Ty>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a,
+                     splits);
+  return hipGetLastError();
 }
 
 template <typename Ty, int MB, int C, int kD, int AI, bool kDma>
@@ -1032,11 +1082,7 @@ hipError_t launch_staged(const Int8Args &a, int splits, hipStream_t s) {
                      dim3((unsigned)(cols * rows), (unsigned)splits), dim3(64 * kW), 0, s, a, cols,
                      splits);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  const long long quads = (long long)a.M * ((a.N + 3) / 4);
-  hipLaunchKernelGGL(int8_join_kernel<Ty>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a,
-                     splits);
-  return hipGetLastError();
+  return e != hipSuccess || splits == 1 ? e : launch_join<Ty>(a, splits, s);
 }
 
 template <typename Ty, bool kDma>
@@ -1075,10 +1121,12 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
   if (kind == kMid || !aligned) {
     const TileOrder order{(a.M + kMM - 1) / kMM, (a.N + kMN - 1) / kMN};
     const long long tiles = (long long)order.ntm * order.ntn;
-    const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds));
-    if (aligned) hipLaunchKernelGGL((int8_mid_kernel<Ty, true>), grid, dim3(512), 0, s, a, order);
-    else hipLaunchKernelGGL((int8_mid_kernel<Ty, false>), grid, dim3(512), 0, s, a, order);
-    return hipGetLastError();
+    const int splits = kind == kMid && a.ws ? mid_shape(a.M, a.K, a.N).splits : 1;
+    const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds), (unsigned)splits);
+    if (aligned) hipLaunchKernelGGL((int8_mid_kernel<Ty, true>), grid, dim3(512), 0, s, a, order, splits);
+    else hipLaunchKernelGGL((int8_mid_kernel<Ty, false>), grid, dim3(512), 0, s, a, order, splits);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_join<Ty>(a, splits, s);
   }
   const TileOrder order{(a.M + kBM - 1) / kBM, (a.N + kBN - 1) / kBN};
   const long long tiles = (long long)order.ntm * order.ntn;
@@ -1092,7 +1140,12 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
 }  // namespace
 
 size_t int8_workspace_bytes(int M, int K, int N) {
-  return staged_bytes(staged_shape(M, K, N), M, N);
+  if (K < 16) return 0;
+  switch (kind_of(M, K, N)) {
+    case kStaged: return sums_bytes(staged_shape(M, K, N).splits, M, N);
+    case kMid: return sums_bytes(mid_shape(M, K, N).splits, M, N);
+    default: return 0;
+  }
 }
 
 hipError_t launch_int8_gemm(const Int8Args &a, int out_dtype, hipStream_t s) {

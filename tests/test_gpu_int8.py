@@ -122,6 +122,15 @@ def test_int8_shares_of_k(M, K, N, out):
     check(M, K, N, out, pad=((-K) % 16, (-K) % 16, 0), ws=False)
 
 
+@pytest.mark.parametrize("M,K,N", [(384, 14336, 2050), (500, 16402, 1025), (385, 30007, 515), (512, 131071, 130)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_int8_shares_of_k_in_large_tiles(M, K, N, out):
+    """128 x 128 tiles in shares, rows and columns that end inside one."""
+    check(M, K, N, out, bias=True, addend=True, pad=((-K) % 16, (-K) % 16, 0))
+    check(M, K, N, out, addend=True, inplace=True, pad=(3, 5, 1), off=(1, 2))
+    check(M, K, N, out, pad=((-K) % 16, (-K) % 16, 0), ws=False)
+
+
 @pytest.mark.parametrize("M,K,N", [(4352, 64, 4352), (4300, 80, 4400), (4352, 40, 4357), (4353, 200, 4352),
                                    (2500, 336, 9000)])
 def test_int8_several_tiles_a_workgroup(M, K, N):
