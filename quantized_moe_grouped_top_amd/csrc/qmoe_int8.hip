@@ -745,15 +745,18 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args p, int sp
 // multiplied; one barrier a stage.  The groups' exact sums meet in LDS.  Without
 // kDma (rows that begin at any byte) a stage passes through registers: fetched
 // two steps before it is written to LDS, which is one before it is read.
-// With `splits` > 1, workgroup (tile, y) contracts the y-th share of k and leaves
+// With more than one share of k, workgroup (tile, y) contracts the y-th and leaves
 // its sums in p.ws for int8_join_kernel.
+struct Shares {
+  int n, each, more;                                  // `each` stages, one more in the first `more`
+};
 constexpr int kMM = 128, kMN = 128;
 constexpr int kMidSlot = (kMM + kMN) * kBK;          // 16 KB
 constexpr int kMidPieces = 4;
 
 template <typename Ty, bool kDma>
 __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, TileOrder order,
-                                                           int splits) {
+                                                           Shares shares) {
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kRing * kMidSlot];
   __shared__ float s_sa[kMM], s_sw[kMN], s_bias[kMN];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -770,8 +773,7 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
 
   // this share's whole stages: group 0 the first half
   const int all = p.K / kBK, y = blockIdx.y;
-  const int from = (int)((long long)all * y / splits);
-  const int whole = (int)((long long)all * (y + 1) / splits) - from;
+  const int from = y * shares.each + min(y, shares.more), whole = shares.each + (y < shares.more);
   const int first = from + (grp ? (whole + 1) / 2 : 0);
   const int mine = grp ? whole / 2 : (whole + 1) / 2, steps = (whole + 1) / 2;
 
@@ -872,7 +874,7 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
   }
   // the last bytes of the rows, straight from memory: fetched here, used at the end
   Frags fe;
-  const bool ends = grp == 1 && y == splits - 1 && p.K > all * kBK;
+  const bool ends = grp == 1 && y == shares.n - 1 && p.K > all * kBK;
   const int ke = all * kBK + 16 * g;
   if (ends) {
 #pragma unroll
@@ -950,7 +952,7 @@ __global__ __launch_bounds__(512, 2) void int8_mid_kernel(const Int8Args p, Tile
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       sum[j] = (grp ? acc[i + 2][j] : acc[i][j]) + part[((other * 2 + i) * 4 + j) * 64 + lane];
-    if (splits > 1) {
+    if (shares.n > 1) {
       const int m = m0 + ml, np = padded_cols(p.N);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -1123,8 +1125,9 @@ hipError_t launch(const Int8Args &a, hipStream_t s) {
     const long long tiles = (long long)order.ntm * order.ntn;
     const int splits = kind == kMid && a.ws ? mid_shape(a.M, a.K, a.N).splits : 1;
     const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds), (unsigned)splits);
-    if (aligned) hipLaunchKernelGGL((int8_mid_kernel<Ty, true>), grid, dim3(512), 0, s, a, order, splits);
-    else hipLaunchKernelGGL((int8_mid_kernel<Ty, false>), grid, dim3(512), 0, s, a, order, splits);
+    const Shares shares{splits, a.K / kBK / splits, a.K / kBK % splits};
+    if (aligned) hipLaunchKernelGGL((int8_mid_kernel<Ty, true>), grid, dim3(512), 0, s, a, order, shares);
+    else hipLaunchKernelGGL((int8_mid_kernel<Ty, false>), grid, dim3(512), 0, s, a, order, shares);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || splits == 1 ? e : launch_join<Ty>(a, splits, s);
   }
