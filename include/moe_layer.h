@@ -46,13 +46,15 @@ extern "C" {
 
 /* Chooses top_k of E experts for every token.  For token t, in order:
  *   scores   s_e from the logits x_e (MOE_SCORE_*)
- *   keys     k_e = s_e + bias[e]; without a bias the logits themselves (the
- *            same order, without its rounding)
+ *   keys     k_e = s_e + bias[e], -inf where the logit is -inf; without a bias
+ *            the logits themselves (the same order, without its rounding)
  *   groups   the E experts are n_group groups of E / n_group neighbours; a
  *            group counts as its largest key (MOE_GROUP_MAX) or as the sum of
- *            its two largest s_e + bias[e] (MOE_GROUP_TOP2); the topk_group
- *            best groups stay (on equal counts the lower group), experts of
- *            the others are never chosen.  n_group = topk_group = 1: no groups
+ *            its two largest keys, without a bias its two largest scores
+ *            (MOE_GROUP_TOP2; a masked expert counts -inf beside a bias, its
+ *            score 0 without one); the topk_group best groups stay (on equal
+ *            counts the lower group), experts of the others are never chosen.
+ *            n_group = topk_group = 1: no groups
  *   choice   the top_k largest keys of those experts, largest first (on equal
  *            keys the lower expert)
  *   weights  w_j = s of the j-th choice (the bias only steers the choice); if
@@ -64,8 +66,9 @@ extern "C" {
  * biases are exactly equal); what groups count is rounded to 38 bits.  Weights
  * are computed in float64 and rounded once to float32.
  * A logit or bias of -inf masks an expert: it is chosen only where fewer than
- * top_k others are left, and a -inf logit has score 0 (in a token without any
- * other logit every softmax score is 0).  A NaN key precedes every number, +inf
+ * top_k others are left in the groups that stay, and a -inf logit, which masks
+ * whatever the expert's bias, has score 0 (in a token without any other logit
+ * every softmax score is 0).  A NaN key precedes every number, +inf
  * the finite keys; a NaN or +inf logit makes the softmax scores of its token
  * NaN.  ids are distinct and inside [0, E) whatever the logits hold.
  *

@@ -57,7 +57,9 @@ def route_general(logits, bias, top_k, score=SOFTMAX, n_group=1, topk_group=1,
     w = np.empty((M, top_k))
     for t in range(M):
         s = _softmax(x[t]) if score == SOFTMAX else _sigmoid(x[t])
-        biased = s if bias is None else s + np.asarray(bias, np.float64)
+        biased = s
+        if bias is not None:                 # a logit of -inf masks its expert, whatever its bias
+            biased = np.where(x[t] == -np.inf, -np.inf, s + np.asarray(bias, np.float64))
         key = x[t] if bias is None else biased
         worth = np.empty(n_group)
         for g in range(n_group):

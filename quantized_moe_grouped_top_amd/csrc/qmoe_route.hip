@@ -404,6 +404,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     for (int u = 0; u < V; ++u) {
       key[u] = finite(key[u]);
       if (top2) sc[u] = finite(sc[u]);
+      if (a.bias && v[u] == -INFINITY) key[u] = sc[u] = -stand_in_inf();   // masked, whatever its bias
     }
   }
 #pragma unroll

@@ -209,6 +209,58 @@ def test_route_many_tokens_of_odd_numbers_of_experts(E, n, keep):
                 assert np.all(np.abs(w[rows] - w0) <= 2.0 ** -23 * w0)
 
 
+# ---- masked experts beside a bias, scores that are no numbers -------------------------
+@pytest.mark.parametrize("M", [40, 8200])
+@pytest.mark.parametrize("E,n,keep,k", [(8, 2, 1, 2), (60, 5, 2, 4), (128, 8, 4, 8), (160, 8, 3, 6),
+                                        (250, 10, 3, 8), (512, 16, 5, 8)])
+def test_route_masked_logits_beside_a_bias(M, E, n, keep, k):
+    """A -inf logit takes its expert out whatever its bias: the choice is the one
+    of the same router without these experts (their softmax terms are exp(-inf) =
+    0).  Both lists of weights are within 2^-23 of the same exact values."""
+    print(f"\n[route] masked beside a bias M={M} E={E}", flush=True)
+    gs = E // n
+    gone = np.sort(np.concatenate([g * gs + np.arange(1, gs // 2 + 1) % gs for g in range(n)]))
+    left = np.setdiff1d(np.arange(E), gone)
+    x = _logits(M, E, "f32", _seed(M, E, "gone"))
+    x[:, left[0]] = -90.0                                         # a sigmoid score near 1e-39
+    x[:, gone] = float("-inf")
+    b = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+    b[gone] = 0.9                                                 # what a balance bias grows to
+    zero = torch.zeros(E)
+    xl = x[:, left].contiguous()
+    few = np.r_[0:30, M - 10:M]
+    for bias in (b, zero):
+        bd, bl = bias.to(DEV), bias[left].contiguous().to(DEV)
+        for score in (0, 1):
+            for groups, rule in ((1, 0), (n, 0), (n, 1)):
+                if rule == 1 and left.size // n < 2:
+                    continue
+                got, w = route(x, "f32", k, bd, score, groups, keep if groups > 1 else 1, rule, True, 2.5)
+                assert not np.isin(got, gone).any(), (score, groups, rule)
+                want, w0 = route(xl, "f32", k, bl, score, groups, keep if groups > 1 else 1, rule, True, 2.5)
+                assert np.array_equal(got, left[want]), (score, groups, rule)
+                assert np.all(np.abs(w.astype(np.float64) - w0) <= 2.0 ** -22 * w0)
+                ids0, _ = L.route_general(x.cpu().numpy()[few], bias.numpy(), k, score, groups,
+                                          keep if groups > 1 else 1, rule, True, 2.5)
+                assert np.array_equal(got[few], ids0)
+
+
+def test_route_fewer_experts_left_than_choices_beside_a_bias():
+    """Masked experts follow the others, lower expert first, with weight 0."""
+    print("\n[route] few left beside a bias", flush=True)
+    for E in (8, 64, 256):
+        x = torch.full((3, E), float("-inf"))
+        x[1, E - 1] = -95.0
+        x[2, 2], x[2, E - 2] = 0.25, -1.0
+        b = torch.linspace(-1.0, 1.0, E)
+        for score in (0, 1):
+            ids, w = route(x.to(DEV), "f32", 4, b.to(DEV), score, renorm=False)
+            assert list(ids[0]) == [0, 1, 2, 3] and list(ids[1]) == [E - 1, 0, 1, 2]
+            assert list(ids[2]) in ([2, E - 2, 0, 1], [E - 2, 2, 0, 1])
+            assert np.all(w[0] == 0) and np.all(w[1:, 2:] == 0) and np.all(w[2, :2] > 0)
+            check_route(x.to(DEV), "f32", 4, b.to(DEV), score)
+
+
 # ---- gradient ----------------------------------------------------------------------
 def _dense_tol(x, ids, g, scale):
     """Bound for the dense softmax gradient in float32.  p = exp(x - m) / Z:

@@ -237,6 +237,23 @@ def test_oracle_route_groups_by_enumeration(score, rule):
 
 
 @pytest.mark.parametrize("score", [L.SOFTMAX, L.SIGMOID])
+def test_oracle_masked_experts_are_not_chosen(score):
+    """A -inf logit takes its expert out whatever its bias: the choice of the
+    router without these experts, which then have no group to lift either."""
+    rng = np.random.default_rng(11)
+    x, b = rng.standard_normal((20, 16)), 0.2 * rng.standard_normal(16)
+    gone = np.array([1, 6, 8, 15])
+    left = np.setdiff1d(np.arange(16), gone)
+    x[:, 0] = -90.0                          # the same sigmoid score as -inf's in most formats
+    x[:, gone], b[gone] = -np.inf, 0.9
+    for n, keep, rule in ((1, 1, L.GROUP_MAX), (4, 2, L.GROUP_MAX), (4, 2, L.GROUP_TOP2)):
+        ids, w = L.route_general(x, b, 4, score, n, keep, rule)
+        want, w0 = L.route_general(x[:, left], b[left], 4, score, n, keep, rule)
+        assert np.array_equal(ids, left[want])
+        np.testing.assert_allclose(w, w0, rtol=1e-12)
+
+
+@pytest.mark.parametrize("score", [L.SOFTMAX, L.SIGMOID])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_oracle_gradient_against_differences(score, renorm):
     rng = np.random.default_rng(7)
