@@ -69,8 +69,8 @@ extern "C" {
  * top_k others are left in the groups that stay, and a -inf logit, which masks
  * whatever the expert's bias, has score 0 (in a token without any other logit
  * every softmax score is 0).  A NaN key precedes every number, +inf
- * the finite keys; a NaN or +inf logit makes the softmax scores of its token
- * NaN.  ids are distinct and inside [0, E) whatever the logits hold.
+ * the finite keys; a NaN or +inf logit makes the softmax scores of its token,
+ * and so its weights, NaN.  ids are distinct and inside [0, E) whatever the logits hold.
  *
  *   logits       [M, E] of type dtype (MOE_F32, MOE_BF16, MOE_F16), rows ld
  *                elements apart (ld >= E), aligned to their type

@@ -74,7 +74,7 @@ def route_general(logits, bias, top_k, score=SOFTMAX, n_group=1, topk_group=1,
         chosen = _ranked(key, pool)[:top_k]
         ids[t] = chosen
         if renormalize and score == SOFTMAX:
-            v = _softmax(x[t, chosen])
+            v = np.full(top_k, np.nan) if np.isnan(s).any() else _softmax(x[t, chosen])
         else:
             v = s[chosen]
             if renormalize:

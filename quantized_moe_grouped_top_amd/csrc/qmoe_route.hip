@@ -496,7 +496,9 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
     if (a.renormalize) {
       m = lanes_max<0, 3>(chosen ? xj : -INFINITY);
       if (m == -INFINITY) m = 0.0f;
-      w = exp((double)xj - (double)m);
+      // z is only summed up where keys rest on scores: NaN then by any expert's
+      // logit, chosen or not.  Elsewhere such a logit is itself chosen.
+      w = z != z ? z : exp((double)xj - (double)m);
     } else {
       w = z == 0.0 ? 0.0 : exp((double)xj - (double)m) / z;
     }

@@ -261,6 +261,27 @@ def test_route_fewer_experts_left_than_choices_beside_a_bias():
             check_route(x.to(DEV), "f32", 4, b.to(DEV), score)
 
 
+@pytest.mark.parametrize("M", [24, 8200])
+def test_route_softmax_with_a_nan_that_is_not_chosen(M):
+    """A NaN or +inf logit makes every softmax score of its token NaN, the
+    renormalised weights of other experts too; other tokens keep theirs."""
+    print(f"\n[route] NaN M={M}", flush=True)
+    for E in (16, 60, 128, 256, 512):
+        x = _logits(M, E, "f32", _seed(M, E, "nan"))
+        x[3, E - 6] = float("nan")
+        x[5, E - 5] = float("inf")
+        x[7, E - 6], x[7, E - 5] = float("nan"), float("-inf")
+        bad = [3, 5, 7]
+        fine = np.setdiff1d(np.arange(M), bad)
+        for bias, groups, rule in ((torch.zeros(E, device=DEV), 1, 0), (None, 4, 1),
+                                   (torch.zeros(E, device=DEV), 4, 1)):
+            for renorm in (True, False):
+                ids, w = route(x, "f32", 4, bias, 0, groups, max(1, groups // 2), rule, renorm, 1.5)
+                assert np.all(np.isnan(w[bad])) and np.all(np.isfinite(w[fine])), (E, groups, renorm)
+                assert np.all((ids >= 0) & (ids < E))
+                check_route(x[:24], "f32", 4, bias, 0, groups, max(1, groups // 2), rule, renorm, 1.5)
+
+
 # ---- gradient ----------------------------------------------------------------------
 def _dense_tol(x, ids, g, scale):
     """Bound for the dense softmax gradient in float32.  p = exp(x - m) / Z:

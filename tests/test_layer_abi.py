@@ -253,6 +253,16 @@ def test_oracle_masked_experts_are_not_chosen(score):
         np.testing.assert_allclose(w, w0, rtol=1e-12)
 
 
+def test_oracle_softmax_scores_of_a_token_with_a_nan():
+    """The weights are NaN whether the NaN or +inf logit's expert is chosen or not."""
+    x = np.zeros((3, 16))
+    x[0, 10], x[1, 10] = np.nan, np.inf
+    for bias in (None, np.zeros(16), 0.1 * np.arange(16.0)):
+        for renorm in (True, False):
+            ids, w = L.route_general(x, bias, 4, L.SOFTMAX, renormalize=renorm)
+            assert np.isnan(w[:2]).all() and np.isfinite(w[2]).all()
+
+
 @pytest.mark.parametrize("score", [L.SOFTMAX, L.SIGMOID])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_oracle_gradient_against_differences(score, renorm):
