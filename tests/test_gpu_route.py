@@ -444,6 +444,69 @@ def test_route_backward_against_differences():
             assert np.abs(diff - dx.cpu().numpy()[0]).max() < 2.0 ** -15 + 2.0 ** -12 * g.abs().max().item()
 
 
+# ---- the plain softmax gradient of confident tokens -----------------------------------
+def _dense_reference(x, ids, g, scale):
+    """Plain softmax gradient of one token in float64 without the difference of
+    nearly equal terms, dx_e = scale p_e (g_e sum_{i != e} p_i - sum_{i != e} g_i p_i),
+    and a bound for its evaluation in float32 in this form.  In half steps
+    (2^-24): x - m carries |x - m| of them into the exponential, its product with
+    log2(e) and that constant 1.5 |x - m|, the exponential 2; sums are pieces
+    of at most 24 and a tree over 64 lanes, at most 30; the division 3; z minus the
+    own term doubles what z carries; products, scale and differences one each: at
+    most 128 without the exponentials."""
+    x, g = x.astype(np.float64), g.astype(np.float64)
+    E = x.size
+    d = x.max() - x
+    p = np.exp(-d)
+    p /= p.sum()
+    up, mag = np.zeros(E), np.zeros(E)
+    for j, e in enumerate(ids):
+        if 0 <= e < E:
+            up[e] += g[j]
+            mag[e] += abs(g[j])
+    own = 2.5 * d + 2
+    out, tol = np.empty(E), np.empty(E)
+    for e in range(E):
+        o = np.arange(E) != e
+        out[e] = scale * p[e] * (up[e] * p[o].sum() - (up[o] * p[o]).sum())
+        terms = (mag[e] + mag[o]) * p[o]
+        tol[e] = scale * p[e] * 2.0 ** -24 * ((128 + own[e]) * terms.sum() + (own[o] * terms).sum())
+    return out, tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E,k", [(8, 8), (24, 3), (60, 6), (128, 8), (200, 8), (256, 8), (512, 8)])
+def test_route_backward_of_confident_tokens(E, k, dtype):
+    """One logit 0 to 30 above the others, chosen in most tokens: its gradient is
+    a small difference of large terms, and holds relative to what is left."""
+    print(f"\n[route backward] confident E={E} k={k} {dtype}", flush=True)
+    gen = torch.Generator().manual_seed(_seed(E, k, dtype))
+    M = 32
+    x = 0.25 * torch.randn(M, E, generator=gen)
+    ids = torch.stack([torch.randperm(E, generator=gen)[:k] for _ in range(M)]).int()
+    for t in range(M):
+        x[t, ids[t, t % k]] = float(t)                            # the t-th token's gap, nearly
+    x[9, ids[9, 0]] = x[9, ids[9, 1]] = 12.0                      # two share the maximum
+    x[10] = -3.0
+    x[10, (int(ids[10].max()) + 1) % E] = 14.0                    # perhaps not chosen
+    ids[11, 1] = ids[11, 11 % k]                                  # the maximum twice
+    ids[12, (12 % k + 1) % k] = -1
+    x = x.to(DT[dtype][1])
+    g = torch.randn(M, k, generator=gen)
+    dx = torch.empty(M, E, dtype=DT[dtype][1], device=DEV)
+    qm.moe_route_topk_backward(g.to(DEV), ids.to(DEV), x.to(DEV), DT[dtype][0], E, M, E, k, 0, False, 2.5,
+                               dx, E)
+    torch.cuda.synchronize()
+    got = dx.double().cpu().numpy()
+    tiny = {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -24}[dtype]
+    eps = torch.finfo(DT[dtype][1]).eps / 2
+    for t in range(M):
+        ref, tol = _dense_reference(x[t].double().numpy(), ids[t].numpy(), g[t].numpy(), 2.5)
+        tol = tol + eps * (np.abs(ref) + tol) + tiny
+        bad = np.abs(got[t] - ref) > tol
+        assert not bad.any(), (t, np.argwhere(bad)[:3], got[t][bad][:3], ref[bad][:3], tol[bad][:3])
+
+
 # ---- alignment ------------------------------------------------------------------------
 def check_align(ids, E, block_m, first=0, counts=True):
     M, k = ids.shape
