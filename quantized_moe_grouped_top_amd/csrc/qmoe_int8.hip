@@ -10,9 +10,12 @@ namespace {
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// One output value from its exact sum.
+// One output value from its exact sum.  Here and in the other epilogues every
+// step is rounded by itself (no multiply-add joins the second scale and the
+// bias), so that all kernels give the same bits.
 template <typename Ty>
 __device__ __forceinline__ void store_one(const Int8Args &p, int m, int n, int sum) {
+#pragma clang fp contract(off)
   float v = (float)sum * p.a_scale[m] * p.w_scale[n];
   if (p.bias) v += p.bias[n];
   const long long i = (long long)m * p.ldo + n;
@@ -111,6 +114,7 @@ template <typename Ty>
 __device__ __forceinline__ void store_run(const Int8Args &p, int m, int n0, int col, int g, float sa,
                                           const float *s_sw, const float *s_bias, const i32x4 &lo,
                                           const i32x4 &hi) {
+#pragma clang fp contract(off)
   typedef typename Ty::T T;
   constexpr bool kWide = sizeof(T) == 4;
   const bool row_ok = m < p.M;
@@ -437,6 +441,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int8_big_kernel(const Int8Args
 template <typename Ty>
 __device__ __forceinline__ void store_four(const Int8Args &p, int m, int n, float sa, const float *sw,
                                            const float *bias, const i32x4 &sum) {
+#pragma clang fp contract(off)
   typedef typename Ty::T T;
   if (m >= p.M) return;
   const long long at = (long long)m * p.ldo + n;

@@ -242,6 +242,32 @@ def test_int8_is_exact_and_repeatable():
             assert np.array_equal(y.cpu().numpy().astype(np.float64), ref)
 
 
+@pytest.mark.parametrize("M,K,N", [(5, 9, 70), (100, 15, 300), (1, 4096, 512), (1, 14336, 256),
+                                   (40, 14336, 130), (64, 640, 1024), (300, 1024, 1100),
+                                   (512, 14336, 1030), (1500, 272, 2100)])
+def test_int8_epilogue_is_float32_in_its_order(M, K, N):
+    """float(sum) * a_scale * w_scale + bias + addend, each step rounded to
+    float32: the same bits from every kernel, with and without the workspace."""
+    print(f"\n[int8] order M={M} K={K} N={N}", flush=True)
+    g = _gen("order", M, K, N)
+    a, w = _codes(M, K, K, 0, g), _codes(N, K, K, 0, g)
+    sa = (torch.rand(M, generator=g) + 0.5).to(DEV) * (1.0 / 128)
+    sw = (torch.rand(N, generator=g) + 0.5).to(DEV) * (1.0 / (128 * K ** 0.5))
+    b, add = torch.randn(N, generator=g).to(DEV), torch.randn(M, N, generator=g).to(DEV)
+    exact = a.cpu().double() @ w.cpu().double().t()               # integers below 2^53
+    base = exact.float() * sa.cpu()[:, None] * sw.cpu()
+    wb = qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N)
+    ws = torch.empty(wb + 16, dtype=torch.uint8, device=DEV)
+    for bias, addend in ((None, None), (b, None), (None, add), (b, add)):
+        want = base if bias is None else base + b.cpu()
+        want = want if addend is None else want + add.cpu()
+        for scratch in (ws, None):
+            y = torch.empty(M, N, device=DEV)
+            qm.moe_gemm_int8w8a8(a, K, sa, w, K, sw, bias, addend, M, K, N, 0, y, N, scratch)
+            torch.cuda.synchronize()
+            assert torch.equal(y.cpu(), want), (bias is not None, addend is not None, scratch is not None)
+
+
 def test_int8_large_output_offsets():
     """Output rows beyond 2^31 elements from the first: 64-bit offsets."""
     print("\n[int8] large output", flush=True)
