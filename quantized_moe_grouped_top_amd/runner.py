@@ -160,6 +160,10 @@ class Int8Linear:
         self.out = _empty((M, N), self.torch_dtype, device)
 
     def quantize(self, x):
+        # M rows of bf16 values, or of their bits as 16-bit integers, without gaps
+        assert x.dtype in (torch.bfloat16, torch.int16, torch.uint16)
+        assert x.shape[-1] == self.K and x.numel() == self.M * self.K and x.is_contiguous()
+        assert x.device == self.a_q.device
         moe_quantize_act(x, self.M, self.K, MOE_Q_INT8_PER_CHANNEL, None, 1, self.a_q,
                          self.a_scale, None, None)
 

@@ -188,6 +188,31 @@ def test_runner_classes_refuse_other_shapes_and_types():
 
 @needs_lib
 @no_gpu
+def test_linear_quantizes_only_its_own_rows(monkeypatch):
+    """What Int8Linear hands to moe_quantize_act, which reads M * K bf16 values from
+    the address it gets: anything else is refused first."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = []
+    monkeypatch.setattr(runner, "moe_quantize_act", lambda *a: calls.append(a))
+    lin = runner.Int8Linear(4, 32, 16, device="cpu")
+    x = torch.zeros(4, 32, dtype=torch.bfloat16)
+    w, s = torch.zeros(16, 32, dtype=torch.int8), torch.zeros(16)
+    for bad in (x.float(), x.half(), x[:3], x[:, :16], torch.zeros(8, 32, dtype=torch.bfloat16)[::2],
+                torch.zeros(32, 4, dtype=torch.bfloat16).t(), x.view(-1), x.to("meta")):
+        with pytest.raises(AssertionError):
+            lin.quantize(bad)
+        with pytest.raises(AssertionError):
+            lin.forward(bad, w, s)
+    assert not calls
+    lin.quantize(x)
+    lin.quantize(x.view(torch.int16))
+    lin.quantize(x.view(2, 2, 32))
+    assert len(calls) == 3
+
+
+@needs_lib
+@no_gpu
 def test_no_tokens_is_valid():
     assert _route(M=0, logits=None, topk_ids=None, topk_weights=None) == qm.MOE_OK
     assert _bwd(M=0, logits=None, d_logits=None) == qm.MOE_OK
