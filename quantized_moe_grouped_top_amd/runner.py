@@ -278,7 +278,12 @@ class RoutedMoE:
     def forward(self, x, logits, w_q, w_scale, bias=None, shared=None):
         """One pass of the hot path; returns the bf16 output bits [M, N] (int16).
         `bias`: the router's balance bias; `shared` = (Int8Linear, w_q, w_scale):
-        a shared expert whose product is added to the routed experts' sum."""
+        a shared expert of the layer's M, K and N whose product is added to the
+        routed experts' sum."""
+        if shared is not None:
+            linear = shared[0]
+            assert (linear.M, linear.K, linear.N) == (self.M, self.K, self.N)
+            assert linear.dtype == MOE_BF16
         self.route(logits, bias)
         self.quantize(x)
         self.gemm(x, w_q, w_scale)

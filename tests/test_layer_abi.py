@@ -213,6 +213,31 @@ def test_linear_quantizes_only_its_own_rows(monkeypatch):
 
 @needs_lib
 @no_gpu
+def test_layer_refuses_a_shared_expert_of_other_sizes(monkeypatch):
+    """Before anything is enqueued: the layer would overwrite its results first."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = []
+    for name in ("moe_align_block_size", "moe_quantize_act", "moe_grouped_gemm_int8w8a8", "moe_combine",
+                 "moe_gemm_int8w8a8"):
+        monkeypatch.setattr(runner, name, lambda *a, name=name: calls.append(name))
+    moe = runner.RoutedMoE("int8dq", 4, 32, 16, 8, 2, device="cpu")
+    x, logits = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(4, 8)
+    w, s = torch.zeros(8, 16, 32, dtype=torch.int8), torch.zeros(8, 16)
+    for M, K, N, out in ((8, 32, 16, "bf16"), (4, 64, 16, "bf16"), (4, 32, 8, "bf16"), (4, 32, 16, "f32"),
+                         (4, 32, 16, "f16")):
+        lin = runner.Int8Linear(M, K, N, out=out, device="cpu")
+        with pytest.raises(AssertionError):
+            moe.forward(x, logits, w, s, shared=(lin, torch.zeros(N, K, dtype=torch.int8), torch.zeros(N)))
+    assert not calls
+    lin = runner.Int8Linear(4, 32, 16, device="cpu")
+    moe.forward(x, logits, w, s, shared=(lin, w[0], s[0]))
+    assert calls == ["moe_align_block_size", "moe_quantize_act", "moe_grouped_gemm_int8w8a8", "moe_combine",
+                     "moe_quantize_act", "moe_gemm_int8w8a8"]
+
+
+@needs_lib
+@no_gpu
 def test_no_tokens_is_valid():
     assert _route(M=0, logits=None, topk_ids=None, topk_weights=None) == qm.MOE_OK
     assert _bwd(M=0, logits=None, d_logits=None) == qm.MOE_OK
