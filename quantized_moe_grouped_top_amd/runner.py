@@ -131,6 +131,10 @@ class TopKRouter:
                        self.renormalize, self.scale, self.topk_ids, self.topk_weights)
 
     def align(self, block_m, sorted_token_ids, expert_ids, num_tokens_post_padded):
+        n = moe_align_max_padded(self.M, self.n_local, self.top_k, block_m)
+        for t, least in ((sorted_token_ids, n), (expert_ids, n // block_m),
+                         (num_tokens_post_padded, 1)):
+            assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= least
         moe_align_topk_ids(self.topk_ids, self.M, self.n_local, self.top_k, block_m,
                            self.expert_first, sorted_token_ids, expert_ids,
                            num_tokens_post_padded, self.expert_counts, self.ws)

@@ -238,6 +238,33 @@ def test_layer_refuses_a_shared_expert_of_other_sizes(monkeypatch):
 
 @needs_lib
 @no_gpu
+def test_router_aligns_into_whole_int32_buffers_only(monkeypatch):
+    """The alignment writes max_padded slots and as many labels as blocks; what
+    cannot hold them is refused first."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = []
+    monkeypatch.setattr(runner, "moe_align_topk_ids", lambda *a: calls.append(a))
+    r = runner.TopKRouter(40, 8, 2, device="cpu")
+    n = qm.moe_align_max_padded(40, 8, 2, 16)
+    i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32)  # noqa: E731
+    good = (i32(n), i32(n // 16), i32(1))
+    for at, bad in ((0, i32(n - 1)), (0, i32(n).long()), (0, i32(2 * n)[::2]), (1, i32(n // 16 - 1)),
+                    (1, i32(n // 16).short()), (1, i32(n // 16, 2)[:, 0]), (2, i32(0)), (2, torch.zeros(1))):
+        buffers = list(good)
+        buffers[at] = bad
+        with pytest.raises(AssertionError):
+            r.align(16, *buffers)
+    with pytest.raises(qm.MoeError):
+        r.align(24, *good)
+    assert not calls
+    r.align(16, *good)
+    r.align(16, i32(n + 5), i32(n), i32(2))
+    assert len(calls) == 2
+
+
+@needs_lib
+@no_gpu
 def test_no_tokens_is_valid():
     assert _route(M=0, logits=None, topk_ids=None, topk_weights=None) == qm.MOE_OK
     assert _bwd(M=0, logits=None, d_logits=None) == qm.MOE_OK
