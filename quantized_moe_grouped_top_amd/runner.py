@@ -116,6 +116,7 @@ class TopKRouter:
         self.group_rule = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}[group_rule]
         self.renormalize, self.scale = renormalize, scale
         self.expert_first, self.n_local = expert_first, E if n_local is None else n_local
+        self.holds_all = expert_first <= 0 and expert_first + self.n_local >= E
         self.topk_ids = _empty((M, top_k), torch.int32, device)
         self.topk_weights = _empty((M, top_k), torch.float32, device)
         self.expert_counts = _empty((self.n_local,), torch.int32, device)
@@ -232,7 +233,7 @@ class RoutedMoE:
             self.router.route(logits, bias)
             self.router.align(self.block_m, self.sorted_token_ids, self.expert_ids,
                               self.num_tokens_post_padded)
-            if self.router.n_local < self.router.E:      # slots of experts elsewhere add nothing
+            if not self.router.holds_all:                # slots of experts elsewhere add nothing
                 self.y.zero_()
             return
         assert bias is None, "a balance bias needs a TopKRouter"

@@ -265,6 +265,25 @@ def test_router_aligns_into_whole_int32_buffers_only(monkeypatch):
 
 @needs_lib
 @no_gpu
+@pytest.mark.parametrize("first,n_local,holds_all", [
+    (0, None, True), (0, 8, True), (0, 4, False), (4, 4, False), (4, None, False), (6, 4, False),
+    (0, 12, True), (-2, 10, True), (-2, 8, False)])
+def test_rows_of_experts_elsewhere_are_cleared_for_every_window(monkeypatch, first, n_local, holds_all):
+    """A window that misses an expert, however many it holds itself: the rows of y
+    that no grouped GEMM writes must not reach the sum."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    for name in ("moe_route_topk", "moe_align_topk_ids"):
+        monkeypatch.setattr(runner, name, lambda *a: None)
+    r = runner.TopKRouter(4, 8, 2, expert_first=first, n_local=n_local, device="cpu")
+    moe = runner.RoutedMoE("int8dq", 4, 32, 16, r.n_local, 2, device="cpu", router=r)
+    moe.y.fill_(7)
+    moe.route(torch.zeros(4, 8))
+    assert torch.all(moe.y == (7 if holds_all else 0))
+
+
+@needs_lib
+@no_gpu
 def test_no_tokens_is_valid():
     assert _route(M=0, logits=None, topk_ids=None, topk_weights=None) == qm.MOE_OK
     assert _bwd(M=0, logits=None, d_logits=None) == qm.MOE_OK
