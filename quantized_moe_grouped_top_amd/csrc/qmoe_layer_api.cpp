@@ -91,7 +91,9 @@ int moe_route_topk_backward(const float *d_weights, const int *topk_ids, const v
 }
 
 size_t moe_align_workspace_bytes(int M, int E, int top_k) {
-  if (M < 0 || E < 1 || E > MOE_MAX_EXPERTS || top_k < 1 || top_k > MOE_MAX_TOPK) return 0;
+  if (M < 0 || E < 1 || E > MOE_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK ||
+      (long long)M * top_k > MOE_MAX_SLOTS)
+    return 0;
   return ((size_t)M * top_k + 1023) / 1024 * E * sizeof(int);
 }
 

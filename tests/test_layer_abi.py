@@ -125,6 +125,16 @@ def test_align_ids_rejects(kw, code):
     assert ei.value.code == code
 
 
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("M,E,top_k", [(8193, 128, 8), (65537, 8, 1), (2147483647, 128, 8), (64, 8, 9),
+                                       (64, 2, 4), (-1, 8, 2), (64, 0, 1), (64, 129, 2), (64, 8, 0)])
+def test_align_workspace_of_refused_sizes_is_0(M, E, top_k):
+    with pytest.raises(qm.MoeError):
+        _align(M=M, E=E, top_k=top_k)
+    assert qm.moe_align_workspace_bytes(M, E, top_k) == 0
+
+
 def _int8(**kw):
     a = dict(a_q=FAKE, lda=64, a_scale=FAKE, w_q=FAKE, ldw=64, w_scale=FAKE, bias=None,
              addend=None, M=4, K=64, N=32, out_dtype=1, out=FAKE, ldo=32, workspace=None, stream=0)
