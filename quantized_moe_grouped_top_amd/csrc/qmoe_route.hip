@@ -1009,9 +1009,15 @@ hipError_t route_with(const RouteArgs &a, int dtype, hipStream_t s) {
     if (a.top_k <= 2) QMOE_ROUTE(2, mode); \
     else QMOE_ROUTE(8, mode);              \
   } while (0)
-  if (!grouped) QMOE_ROUTE_K(kNoGroups);
-  else if (by_lanes) QMOE_ROUTE_K(kLaneGroups);
-  else QMOE_ROUTE_K(kAnyGroups);
+  if (!grouped) {
+    QMOE_ROUTE_K(kNoGroups);
+  } else if (by_lanes) {
+    QMOE_ROUTE_K(kLaneGroups);
+  } else if constexpr (V <= 8) {         // launch_route_topk's wider lanes take no others
+    QMOE_ROUTE_K(kAnyGroups);
+  } else {
+    return hipErrorInvalidValue;
+  }
 #undef QMOE_ROUTE_K
 #undef QMOE_ROUTE
   return hipGetLastError();
