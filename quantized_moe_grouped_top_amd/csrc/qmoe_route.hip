@@ -803,7 +803,6 @@ __device__ __forceinline__ void padded_starts(const int *s_cnt, int E, int block
   const int half = __shfl(x0, 63);
   if (lane < E) s_off[lane] = x0 - c0;
   if (lane + 64 < E) s_off[lane + 64] = half + x1 - c1;
-  if (lane == 0) s_off[E] = 0;
   const int total = half + __shfl(x1, 63);
   if (lane == 0) s_off[E] = total;
 }
