@@ -23,17 +23,13 @@ __device__ __forceinline__ void store_one(const Int8Args &p, int m, int n, int s
   ((typename Ty::T *)p.out)[i] = Ty::store(v);
 }
 
-// 16 bytes of a row from byte k on: zero past K, any alignment.
-__device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else {
-    uint8_t b[16];
+// A row of K < 16 bytes, any alignment, with zeros behind it.
+__device__ __forceinline__ i32x4 load_short(const int8_t *row, int K) {
+  uint8_t b[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = k + i < K ? (uint8_t)row[k + i] : 0;
-    __builtin_memcpy(&v, b, 16);
-  }
+  for (int i = 0; i < 16; ++i) b[i] = i < K ? (uint8_t)row[i] : 0;
+  i32x4 v;
+  __builtin_memcpy(&v, b, 16);
   return v;
 }
 
@@ -58,45 +54,42 @@ __device__ __forceinline__ i32x4 load_end(const int8_t *row, int k, int K) {
 }
 
 // K below 16 (the kernels below move 16 bytes of a row at a time): 64 x 64 tiles,
-// four wavefronts of 32 x 32, byte by byte into LDS rows of 80 bytes, one product
-// of 32 k (v_mfma_i32_32x32x32_i8, weights as the first operand).
-constexpr int kShortRow = 80;
+// four wavefronts of 32 x 32, rows byte by byte into LDS, 48 bytes apart, and one
+// product of 32 k (v_mfma_i32_32x32x32_i8), the second sixteen zeros.  The weights
+// are the second operand here: neighbouring lanes then hold, and store one by one,
+// neighbouring columns (4096 x 8 x 28672 bf16 91 us, the other way round 284; bound
+// by those stores).
+constexpr int kShortRow = 48;
 constexpr long long kShortGrid = 1 << 20;
 template <typename Ty>
 __global__ __launch_bounds__(256) void int8_short_kernel(const Int8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[64 * kShortRow], s_w[64 * kShortRow];
+  __shared__ __attribute__((aligned(16))) uint8_t s_rows[128 * kShortRow];   // activations, weights
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = tid >> 2, c = (tid & 3) * 16;        // this thread's row and chunk of a stage
+  const int r = (tid >> 1) & 63, c = tid & 1;        // this thread's row and half of it
+  const bool of_w = tid >= 128;
   const int g = lane >> 5, q = lane & 31;
   const int mw = (wave & 1) * 32, nw = (wave >> 1) * 32;
   const long long ntn = (p.N + 63) / 64, tiles = (p.M + 63ll) / 64 * ntn;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int m0 = (int)(t / ntn) * 64, n0 = (int)(t % ntn) * 64;
-    const bool am = r < p.M - m0, wn = r < p.N - n0;
-    const int8_t *ar = p.a + (long long)(am ? m0 + r : 0) * p.lda;
-    const int8_t *wr = p.w + (long long)(wn ? n0 + r : 0) * p.ldw;
+    i32x4 v = {0, 0, 0, 0};
+    if (c == 0) {
+      if (!of_w && r < p.M - m0) v = load_short(p.a + (long long)(m0 + r) * p.lda, p.K);
+      if (of_w && r < p.N - n0) v = load_short(p.w + (long long)(n0 + r) * p.ldw, p.K);
+    }
+    __syncthreads();                                 // the tile before has been read
+    *reinterpret_cast<i32x4 *>(s_rows + (tid >> 1) * kShortRow + 16 * c) = v;
+    __syncthreads();
+    const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_rows + (mw + q) * kShortRow + 16 * g);
+    const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_rows + (64 + nw + q) * kShortRow + 16 * g);
     i32x16 acc;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0;
-    for (int k = 0; k < p.K; k += 64) {
-      const i32x4 z = {0, 0, 0, 0};
-      const i32x4 av = am ? load16(ar, k + c, p.K) : z;
-      const i32x4 wv = wn ? load16(wr, k + c, p.K) : z;
-      __syncthreads();
-      *reinterpret_cast<i32x4 *>(s_a + r * kShortRow + c) = av;
-      *reinterpret_cast<i32x4 *>(s_w + r * kShortRow + c) = wv;
-      __syncthreads();
+    for (int e = 0; e < 16; ++e) acc[e] = 0;
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa, fw, acc, 0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const i32x4 fa = *reinterpret_cast<const i32x4 *>(s_a + (mw + q) * kShortRow + 32 * h + 16 * g);
-        const i32x4 fw = *reinterpret_cast<const i32x4 *>(s_w + (nw + q) * kShortRow + 32 * h + 16 * g);
-        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, fa, acc, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int ml = mw + q, nl = nw + 8 * (v >> 2) + 4 * g + (v & 3);
-      if (ml < p.M - m0 && nl < p.N - n0) store_one<Ty>(p, m0 + ml, n0 + nl, acc[v]);
+    for (int e = 0; e < 16; ++e) {
+      const int ml = mw + 8 * (e >> 2) + 4 * g + (e & 3), nl = nw + q;
+      if (ml < p.M - m0 && nl < p.N - n0) store_one<Ty>(p, m0 + ml, n0 + nl, acc[e]);
     }
   }
 }

@@ -146,6 +146,15 @@ def test_int8_ends_of_rows(K):
         check(M, K, N, "f32", pad=(1, 1, 0), off=(1, 1))
 
 
+@pytest.mark.parametrize("K", [1, 2, 7, 8, 15])
+@pytest.mark.parametrize("M,N", [(1, 1), (63, 65), (64, 64), (130, 300), (1000, 70)])
+def test_int8_rows_shorter_than_16(M, K, N):
+    """The kernel of short rows: tiles that end inside rows and columns, rows at any
+    byte, what lies behind the K bytes not read into the sums."""
+    check(M, K, N)
+    check(M, K, N, "f32", bias=True, addend=True, pad=(16 - K, 3, 1), off=(3, 1), ws=False)
+
+
 def test_int8_two_streams():
     """Two calls at once, each with its own workspace, on two streams."""
     print("\n[int8] two streams", flush=True)
