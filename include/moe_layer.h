@@ -150,7 +150,7 @@ int moe_align_topk_ids(const int *topk_ids, int M, int E, int top_k, int block_m
  * ======================================================================== */
 
 /* Bytes of device workspace moe_gemm_int8w8a8 can use for this shape (at most
- * 64 MiB; 0 where it needs none or the sizes are invalid).  It splits the
+ * 16 MiB; 0 where it needs none or the sizes are invalid).  It splits the
  * contraction over more workgroups where the output alone has too few. */
 size_t moe_gemm_int8w8a8_workspace_bytes(int M, int K, int N);
 

@@ -51,6 +51,22 @@ def test_layer_sizes():
     assert qm.moe_gemm_int8w8a8_workspace_bytes(4, 1 << 20, 64) == 0
 
 
+@needs_lib
+def test_int8_workspace_holds_the_shares_and_is_at_most_16_mib():
+    """One int32 sum of every output and share, columns padded to four: a share of 2048 k
+    at least in 16-row tiles (14336 / 2048 = 7), 256 CUs over 64 tiles of 64 x 16, all
+    shares of a XCD's 128 x 128 tiles on its 32 CUs (16 tiles: 2), at most 16; 256
+    tiles of 128 x 128 are 2^24 bytes."""
+    for M, K, N, shares in [(1, 14336, 64, 7), (64, 14336, 1024, 4), (512, 14336, 4096, 2),
+                            (512, 131071, 130, 16), (4096, 14336, 4096, 0), (16, 64, 16, 0), (1, 15, 4096, 0)]:
+        assert qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N) == shares * M * ((N + 3) // 4 * 4) * 4, (M, K, N)
+    rng = np.random.default_rng(0)
+    for _ in range(4000):
+        M, K, N = (int(2.0 ** v) for v in rng.uniform((0, 0, 0), (18, 16.99, 18)))
+        n = qm.moe_gemm_int8w8a8_workspace_bytes(M, K, N)
+        assert 0 <= n <= 16 << 20 and n % (M * ((N + 3) // 4 * 4) * 4) == 0, (M, K, N)
+
+
 def _route(**kw):
     a = dict(logits=FAKE, dtype=0, ld=128, bias=FAKE, M=16, E=128, top_k=8, score=1, n_group=8,
              topk_group=4, group_rule=1, renormalize=1, scale=2.5, topk_ids=FAKE,
