@@ -65,7 +65,6 @@ int moe_route_topk(const void *logits, int dtype, long long ld, const float *bia
               aligned4(topk_weights),
           MOE_EINVAL, "%s: a pointer is not aligned to its type", fn);
   const RouteArgs a{logits, ld, bias, M, E, top_k, score, n_group,
-                    // all groups kept: the group stage chooses nothing
                     topk_group, group_rule, renormalize != 0, scale, topk_ids, topk_weights};
   return hip_status(launch_route_topk(a, dtype, stream), fn);
 }
