@@ -522,6 +522,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
 // choice instead, in their order.  The plain softmax reads the whole row for its
 // scores, the others only the chosen logits.
 //
+// Renormalised, q_j = s_j / S: dx_j = scale q_j t_j (g_j sum_{i != j} q_i - sum_{i != j}
+// g_i q_i) in float64, t_j = 1 (softmax) or 1 - s_j (sigmoid).
 // Plain softmax: dx_e = scale p_e (g_e - sum_i g_i p_i), in float32 without its
 // cancellation where one score is nearly 1:
 //   chosen e  scale p_e (g_e sum_{i != e} p_i - sum_{i != e} g_i p_i)
@@ -572,10 +574,11 @@ __device__ __forceinline__ void store_values(void *base, long long row_at, int d
 
 // Lanes 0 .. 7 of a token: the sum over the other seven (others), and over all
 // eight (all).
-__device__ __forceinline__ void sums_of_eight(float x, float &others, float &all) {
+template <typename T>
+__device__ __forceinline__ void sums_of_eight(T x, T &others, T &all) {
   others = lane_partner<0>(x);
   all = x + others;
-  float o = lane_partner<1>(all);
+  T o = lane_partner<1>(all);
   others += o;
   all += o;
   o = lane_partner<2>(all);
@@ -709,10 +712,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
       tail = 1.0 / (1.0 + exp((double)x));
     }
     double c = (double)g;
-    if (a.renormalize) {
+    if (a.renormalize) {                            // as above: no sum has the choice's own term
       const double sum = lanes_sum<0, 3>(s);
       s = sum == 0.0 ? 0.0 : s / sum;
-      c -= lanes_sum<0, 3>((double)g * s);
+      double other_s, other_gs, all;
+      sums_of_eight(s, other_s, all);
+      sums_of_eight((double)g * s, other_gs, all);
+      c = c * other_s - other_gs;
     }
     d = (float)((double)a.scale * s * c * tail);
   }

@@ -507,6 +507,46 @@ def test_route_backward_of_confident_tokens(E, k, dtype):
         assert not bad.any(), (t, np.argwhere(bad)[:3], got[t][bad][:3], ref[bad][:3], tol[bad][:3])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E,k", [(8, 8), (60, 3), (128, 8), (512, 2)])
+def test_route_backward_of_confident_renormalised_tokens(E, k, dtype):
+    """Renormalised weights of which one is nearly 1.  dx_j = scale ds_j/dx_j (g_j
+    sum_{i != j} s_i - sum_{i != j} g_i s_i) / S^2 has no difference of nearly
+    equal terms; in float64 it holds to 2^-45 of the terms' magnitude
+    (some ten roundings of 2^-53, the exponentials included), then the result is
+    rounded to float32 and to its type."""
+    print(f"\n[route backward] confident, renormalised E={E} k={k} {dtype}", flush=True)
+    gen = torch.Generator().manual_seed(_seed(E, k, dtype, "renorm"))
+    M = 40
+    ids = torch.stack([torch.randperm(E, generator=gen)[:k] for _ in range(M)]).int()
+    g = torch.randn(M, k, generator=gen)
+    eps = torch.finfo(DT[dtype][1]).eps / 2 + 2.0 ** -24
+    tiny = {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -24}[dtype]
+    for score in (0, 1):
+        x = 0.25 * torch.randn(M, E, generator=gen) - (6.0 if score else 0.0)
+        for t in range(M):                                        # gaps from 0 to 39
+            x[t, ids[t, t % k]] = float(t) if score == 0 else 2.0
+            if score:
+                x[t, ids[t][torch.arange(k) != t % k].long()] -= float(t) - 8.0
+        x = x.to(DT[dtype][1])
+        dx = torch.empty(M, E, dtype=DT[dtype][1], device=DEV)
+        qm.moe_route_topk_backward(g.to(DEV), ids.to(DEV), x.to(DEV), DT[dtype][0], E, M, E, k, score, True,
+                                   2.5, dx, E)
+        torch.cuda.synchronize()
+        got = np.take_along_axis(dx.double().cpu().numpy(), ids.numpy().astype(np.int64), 1)
+        v = np.take_along_axis(x.double().numpy(), ids.numpy().astype(np.int64), 1)
+        gd = g.double().numpy()
+        for t in range(M):
+            s = np.exp(v[t] - v[t].max()) if score == 0 else 1.0 / (1.0 + np.exp(-v[t]))
+            slope = s if score == 0 else s / (1.0 + np.exp(v[t]))
+            for j in range(k):
+                o = np.arange(k) != j
+                c = 2.5 * slope[j] / s.sum() ** 2
+                ref = c * ((gd[t, j] - gd[t, o]) * s[o]).sum()
+                mag = c * ((abs(gd[t, j]) + abs(gd[t, o])) * s[o]).sum()
+                assert abs(got[t, j] - ref) <= eps * abs(ref) + 2.0 ** -45 * mag + tiny, (score, t, j)
+
+
 # ---- alignment ------------------------------------------------------------------------
 def check_align(ids, E, block_m, first=0, counts=True):
     M, k = ids.shape
