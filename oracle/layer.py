@@ -25,8 +25,8 @@ def _softmax(v):
 
 
 def _sigmoid(v):
-    with np.errstate(over="ignore"):
-        return 1.0 / (1.0 + np.exp(-v))
+    e = np.exp(-np.abs(v))                   # does not overflow
+    return np.where(np.asarray(v) < 0, e, 1.0) / (1.0 + e)
 
 
 def _to_38_bits(v):

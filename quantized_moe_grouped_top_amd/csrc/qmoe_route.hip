@@ -204,7 +204,12 @@ __device__ __forceinline__ double sigmoid_key(float x, double lead) {
   return fma(y, fma(-d, y, 1.0), y);
 }
 
-__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// The score and 1 - score, by the exponential that cannot overflow.
+__device__ __forceinline__ double sigmoid64(double x, double &rest) {
+  const double e = exp(-__builtin_fabs(x)), d = 1.0 / (1.0 + e), small = e * d;
+  rest = x < 0.0 ? d : small;
+  return x < 0.0 ? small : d;
+}
 
 // ---- router: sorted lists ------------------------------------------------------------
 // Larger and smaller of two keys (never NaN).  As instructions: the compiler's
@@ -503,7 +508,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
       w = z == 0.0 ? 0.0 : exp((double)xj - (double)m) / z;
     }
   } else {
-    w = sigmoid64((double)xj);
+    double rest;
+    w = sigmoid64((double)xj, rest);
   }
   if (a.renormalize) {
     const double sum = lanes_sum<0, 3>(chosen ? w : 0.0);
@@ -708,8 +714,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
       if (m == -INFINITY) m = 0.0f;
       if (valid) s = exp((double)x - (double)m);
     } else if (valid) {
-      s = sigmoid64((double)x);
-      tail = 1.0 / (1.0 + exp((double)x));
+      s = sigmoid64((double)x, tail);
     }
     double c = (double)g;
     if (a.renormalize) {                            // as above: no sum has the choice's own term

@@ -547,6 +547,27 @@ def test_route_backward_of_confident_renormalised_tokens(E, k, dtype):
                 assert abs(got[t, j] - ref) <= eps * abs(ref) + 2.0 ** -45 * mag + tiny, (score, t, j)
 
 
+def test_route_backward_of_sigmoid_scores_near_the_smallest_float64():
+    """Equal logits down to -745, where a score is the smallest float64: every choice
+    has 1 / k of their sum.  (exp(-x) alone overflows below -709.)"""
+    print("\n[route backward] smallest scores", flush=True)
+    g = torch.randn(4, 4, generator=torch.Generator().manual_seed(8))
+    x = torch.tensor([-700.0, -715.0, -740.0, -60000.0])[:, None].repeat(1, 16)
+    ids = torch.tensor([[3, 0, 15, 7]]).repeat(4, 1).int()
+    dx = torch.empty(4, 16, device=DEV)
+    qm.moe_route_topk_backward(g.to(DEV), ids.to(DEV), x.to(DEV), 0, 16, 4, 16, 4, 1, True, 1.5, dx, 16)
+    torch.cuda.synchronize()
+    gd = g.double()
+    want = torch.zeros(4, 16, dtype=torch.float64)
+    want[:3].scatter_(1, ids[:3].long(), 1.5 * 0.25 * (gd - gd.mean(1, keepdim=True))[:3])
+    # three roundings of 2^-53 and those to float32
+    assert torch.all((dx.cpu().double() - want).abs() <= 2.0 ** -23 * want.abs() + 2.0 ** -48)
+    got, w = route(x.to(DEV), "f32", 4, None, 1, renorm=True, scale=1.5)
+    assert np.all(got == np.arange(4)) and np.all(w[:3] == np.float32(0.375)) and np.all(w[3] == 0)
+    check_route(x.to(DEV), "f32", 4, None, 1)
+    check_backward(x[:2].to(DEV), "f32", ids[:2].to(DEV), g[:2].to(DEV), 1, True, 1.5)
+
+
 # ---- alignment ------------------------------------------------------------------------
 def check_align(ids, E, block_m, first=0, counts=True):
     M, k = ids.shape
