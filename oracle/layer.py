@@ -107,13 +107,13 @@ def route_backward(d_weights, ids, logits, score=SOFTMAX, renormalize=True, scal
                 out[t] -= scale * u * _softmax(x[t])
         else:
             s = _sigmoid(x[t, c])
-            slope = s * _sigmoid(-x[t, c])
             if renormalize:
                 total = s.sum()
                 if total == 0:
                     continue
-                g = (g - (g * s).sum() / total) / total
-            np.add.at(out[t], c, scale * g * slope)
+                s = s / total                # not g / total: that overflows
+                g = g - (g * s).sum()
+            np.add.at(out[t], c, scale * g * s * _sigmoid(-x[t, c]))
     return out
 
 

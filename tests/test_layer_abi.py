@@ -409,6 +409,15 @@ def test_oracle_gradient_against_differences(score, renorm):
             assert abs((value(x + d) - value(x - d)) / (2 * h) - got[t, e]) < 1e-8
 
 
+def test_oracle_gradient_of_the_smallest_sigmoid_scores():
+    g = np.array([[1.0, -2.0, 0.5]])
+    for v in (-700.0, -715.0, -740.0):
+        got = L.route_backward(g, np.array([[2, 0, 5]]), np.full((1, 8), v), L.SIGMOID, True, 1.5)
+        want = np.zeros((1, 8))
+        want[0, [2, 0, 5]] = 0.5 * (g[0] - g[0].mean())
+        np.testing.assert_allclose(got, want, rtol=1e-12)
+
+
 def test_oracle_align_ids():
     rng = np.random.default_rng(1)
     ids = rng.integers(0, 8, (37, 2)).astype(np.int32)
