@@ -98,8 +98,8 @@ int moe_route_topk(const void *logits, int dtype, long long ld, const float *bia
  *   plain softmax          dx_e = scale p_e (g_e [e chosen] - sum_i g_i p_i)
  * and 0 for every other expert: d_logits is written in full, in the type of
  * the logits.  The scores are computed again from the logits: in float64 where
- * only the chosen ones count, in float32 for the plain softmax, there without
- * the difference g_e - sum_i g_i p_i of nearly equal terms where p_e is nearly 1.
+ * only the chosen ones count, in float32 for the plain softmax, where
+ * no difference g_e - sum_i g_i p_i of nearly equal terms stands for a p_e near 1.
  * Ids outside [0, E) are no choice: they take no part.  An id that stands
  * twice in a token counts twice, in the sums and in its gradient.  A token
  * whose chosen scores are all 0 gets gradient 0.

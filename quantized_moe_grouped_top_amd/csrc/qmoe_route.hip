@@ -525,19 +525,17 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const RouteArgs a, int 
 // One token per G lanes.  Lane j takes the j-th choice and its share of the sums
 // and puts its gradient into the token's row in LDS; then every lane stores the V
 // gradients of its experts.  A token with one expert twice is gathered choice by
-// choice instead, in their order.  The plain softmax reads the whole row for its
-// scores, the others only the chosen logits.
+// choice instead, in their order; the plain softmax, which reads the whole row for
+// its scores, joins such choices first.  The others read only the chosen logits.
 //
 // Renormalised, q_j = s_j / S: dx_j = scale q_j t_j (g_j sum_{i != j} q_i - sum_{i != j}
 // g_i q_i) in float64, t_j = 1 (softmax) or 1 - s_j (sigmoid).
-// Plain softmax: dx_e = scale p_e (g_e - sum_i g_i p_i), in float32 without its
-// cancellation where one score is nearly 1:
-//   chosen e  scale p_e (g_e sum_{i != e} p_i - sum_{i != e} g_i p_i)
-//   others   -scale p_e sum_i g_i p_i
-// The choices' sums are summed without e; of the scores the whole less e loses
-// nothing below one half, and above (z < 2, where exp(m - m) = 1 is the largest
-// term) the rest is summed again without it (16384 x 256 bf16 tokens in the caches:
-// 6.9 us, done in every token 7.9).
+// Plain softmax: dx_e = scale p_e (g_e - sum_i g_i p_i) in float32, but of a chosen
+// expert with a score above one half, where that would be a difference of nearly
+// equal terms,
+//   dx_e = scale p_e (g_e sum_{i != e} p_i - sum_{i != e} g_i p_i),
+// its sums taken without e.  Only a wavefront with such a token does that (16384 x
+// 256 bf16 in the caches: 6.8 us, 7.2 where every token is one).
 template <int V>
 __device__ __forceinline__ void store_values(void *base, long long row_at, int dtype, bool vec,
                                              int e0, int E, const float (&v)[V]) {
@@ -621,7 +619,8 @@ __device__ __forceinline__ void join_twins(int i, int id, float g, int &first_id
 }
 
 // exp(x - m).  The difference comes first: m log2(e) alone overflows where a whole
-// row holds its type's lowest value.
+// row holds its type's lowest value.  Off by up to about 2 + 2.5 |x - m| half steps
+// (2^-24): the difference, its product and log2(e) itself are rounded to float32.
 __device__ __forceinline__ float exp_less(float x, float m) {
   constexpr float kL = 1.44269504f;
   return __builtin_amdgcn_exp2f((x - m) * kL);
@@ -684,29 +683,21 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
     }
     z = lanes_sum<0, kSteps>(z);
     const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-    float rest = z - 1.0f;                          // all scores but one of the largest
-    if (__any(z < 2.0f)) {
-      float below = 0.0f;
-      int tops = 0;
+    const float ej = valid ? exp_less(x, m) : 0.0f;
+    const float gp = g * (ej * inv);
+    none = -a.scale * lanes_sum<0, kSteps>(gp);
+    d = a.scale * g + none;
+    const bool steep = z < 2.0f;                    // the one exponential that is 1 takes over half
+    if (__any(steep)) {
+      float rest = 0.0f, others, all;
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const bool top = p[u] == 1.0f;
-        below += top ? 0.0f : p[u];
-        tops += top;
-      }
-      // one of the largest is not part of the rest: one of the first lane's that has any
-      const unsigned long long with = __ballot(tops > 0) >> first;
-      if (tops > 0 && __builtin_ctzll(with | (1ull << 63)) == i) tops -= 1;
-      rest = lanes_sum<0, kSteps>(below + (float)tops);
+      for (int u = 0; u < V; ++u) rest += p[u] == 1.0f ? 0.0f : p[u];
+      rest = lanes_sum<0, kSteps>(rest);
+      sums_of_eight(gp, others, all);
+      if (steep && ej == 1.0f) d = a.scale * (g * (rest * inv) - others);
     }
 #pragma unroll
     for (int u = 0; u < V; ++u) p[u] *= inv;
-    const float ej = valid ? exp_less(x, m) : 0.0f;
-    const float left = (ej == 1.0f ? rest : z - ej) * inv;   // the other experts' scores
-    float others, all;
-    sums_of_eight(g * (ej * inv), others, all);
-    d = a.scale * (g * left - others);
-    none = -a.scale * lanes_sum<3, kSteps>(all);
   } else {
     double s = 0.0, tail = 1.0;
     if (soft) {
@@ -717,7 +708,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteBwdArgs 
       s = sigmoid64((double)x, tail);
     }
     double c = (double)g;
-    if (a.renormalize) {                            // as above: no sum has the choice's own term
+    if (a.renormalize) {
       const double sum = lanes_sum<0, 3>(s);
       s = sum == 0.0 ? 0.0 : s / sum;
       double other_s, other_gs, all;
