@@ -68,9 +68,9 @@ extern "C" {
  * A logit or bias of -inf masks an expert: it is chosen only where fewer than
  * top_k others are left in the groups that stay, and a -inf logit, which masks
  * whatever the expert's bias, has score 0 (in a token without any other logit
- * every softmax score is 0).  A NaN key precedes every number, +inf
- * the finite keys; a NaN or +inf logit makes the softmax scores of its token,
- * and so its weights, NaN.  ids are distinct and inside [0, E) whatever the logits hold.
+ * every softmax score is 0).  A NaN key precedes every number, +inf the finite
+ * keys; a NaN or +inf logit makes the softmax scores of its token, and so its
+ * weights, NaN.  ids are distinct and inside [0, E) whatever the logits hold.
  *
  *   logits       [M, E] of type dtype (MOE_F32, MOE_BF16, MOE_F16), rows ld
  *                elements apart (ld >= E), aligned to their type
@@ -98,8 +98,9 @@ int moe_route_topk(const void *logits, int dtype, long long ld, const float *bia
  *   plain softmax          dx_e = scale p_e (g_e [e chosen] - sum_i g_i p_i)
  * and 0 for every other expert: d_logits is written in full, in the type of
  * the logits.  The scores are computed again from the logits: in float64 where
- * only the chosen ones count, in float32 for the plain softmax, where
- * no difference g_e - sum_i g_i p_i of nearly equal terms stands for a p_e near 1.
+ * only the chosen ones count, in float32 for the plain softmax; where one score
+ * is nearly all of the sum its difference to the weighted mean is taken over the
+ * others alone, so that it holds relative to what is left.
  * Ids outside [0, E) are no choice: they take no part.  An id that stands
  * twice in a token counts twice, in the sums and in its gradient.  A token
  * whose chosen scores are all 0 gets gradient 0.
