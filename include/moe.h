@@ -478,5 +478,6 @@ int moe_combine(const uint16_t *y, int M, int N, int top_k, uint16_t *out,
 #endif
 
 #include "moe_layer.h"  /* the general router, the alignment of given ids, the dense int8 product */
+#include "moe_block.h"  /* the experts' gated feed-forward in 16 bits, low-rank adapters, the block's norms */
 
 #endif /* QMOE_MOE_H */

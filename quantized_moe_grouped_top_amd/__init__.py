@@ -29,6 +29,10 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_MAX_ROUTE_EXPERTS, MOE_MAX_ROUTE_GROUPS, MOE_MAX_ROUTE_TOKENS = 512, 64, 1 << 25
 MOE_MAX_INT8_K, MOE_MAX_INT8_ROWS = 131071, 1 << 27
+MOE_GATED_SILU, MOE_GATED_GELU = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
+MOE_MAX_BLOCK_ROWS, MOE_MAX_BLOCK_WIDTH, MOE_MAX_LORA_RANK = 1 << 24, 1 << 20, 128
+MOE_MAX_NORM_COLUMNS, MOE_MAX_NORM_ROWS = 16384, 1 << 24
 
 EXPORTS = [
     "moe_last_error", "moe_last_hip_error", "moe_align_max_padded", "moe_recommended_block_m",
@@ -46,6 +50,13 @@ EXPORTS = [
 LAYER_EXPORTS = [
     "moe_route_topk", "moe_route_topk_backward", "moe_align_workspace_bytes",
     "moe_align_topk_ids", "moe_gemm_int8w8a8_workspace_bytes", "moe_gemm_int8w8a8",
+]
+
+# declared in include/moe_block.h (which moe.h includes)
+BLOCK_EXPORTS = [
+    "moe_gated_up", "moe_grouped_linear", "moe_gated_down_backward", "moe_grouped_linear_dgrad",
+    "moe_grouped_linear_wgrad", "moe_lora_workspace_bytes", "moe_lora_add", "moe_norm_residual",
+    "moe_norm_backward_workspace_bytes", "moe_norm_residual_backward",
 ]
 
 
@@ -94,6 +105,19 @@ _SIGS = {
     "moe_align_topk_ids": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "moe_gemm_int8w8a8_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
     "moe_gemm_int8w8a8": (_I, [_P, _L, _P, _P, _L, _P, _P, _P, _I, _I, _I, _I, _P, _L, _P, _P]),
+    "moe_gated_up": (_I, [_P, _L, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_linear": (_I, [_P, _L, _P, _I, _P, _I, _I, _I, _I, _P, _L, _P]),
+    "moe_gated_down_backward": (_I, [_P, _L, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_linear_dgrad": (_I, [_P, _L, _P, _I, _P, _I, _I, _I, _I, _P, _L, _P]),
+    "moe_grouped_linear_wgrad": (_I, [_P, _L, _P, _L, _I, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_lora_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "moe_lora_add": (_I, [_P, _L, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P,
+                          _I, _P, _L, _P, _P]),
+    "moe_norm_residual": (_I, [_P, _I, _I, _P, _I, _P, _P, _I, _F, _F, _P, _F, _I, _I, _P, _P, _P,
+                               _P, _P]),
+    "moe_norm_backward_workspace_bytes": (ctypes.c_size_t, [_I, _I]),
+    "moe_norm_residual_backward": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _F, _F, _P, _P, _P,
+                                        _I, _I, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -355,3 +379,74 @@ def moe_gemm_int8w8a8(a_q, lda, a_scale, w_q, ldw, w_scale, bias, addend, M, K, 
         "moe_gemm_int8w8a8", (a_q, a_scale, w_q, w_scale, bias, addend, out, workspace))
     return _enqueue((_lib or lib()).moe_gemm_int8w8a8, dev, stream, a, lda, sa, w, ldw, sw, b, c, M, K,
                     N, out_dtype, o, ldo, ws)
+
+
+# ---- the block around the experts ---------------------------------------------------
+def moe_gated_up(x, ldx, w, dtype, m_offsets, rows, K, H, E, act, gu, h, stream=None):
+    dev, (x, w, o, gu, h) = _pointers("moe_gated_up", (x, w, m_offsets, gu, h))
+    return _enqueue((_lib or lib()).moe_gated_up, dev, stream, x, ldx, w, dtype, o, rows, K, H, E,
+                    act, gu, h)
+
+
+def moe_grouped_linear(x, ldx, w, dtype, m_offsets, rows, K, N, E, y, ldy, stream=None):
+    dev, (x, w, o, y) = _pointers("moe_grouped_linear", (x, w, m_offsets, y))
+    return _enqueue((_lib or lib()).moe_grouped_linear, dev, stream, x, ldx, w, dtype, o, rows, K, N,
+                    E, y, ldy)
+
+
+def moe_gated_down_backward(dy, lddy, w, gu, dtype, m_offsets, rows, N, H, E, act, dgu, h,
+                            stream=None):
+    dev, (dy, w, gu, o, dgu, h) = _pointers("moe_gated_down_backward",
+                                            (dy, w, gu, m_offsets, dgu, h))
+    return _enqueue((_lib or lib()).moe_gated_down_backward, dev, stream, dy, lddy, w, gu, dtype, o,
+                    rows, N, H, E, act, dgu, h)
+
+
+def moe_grouped_linear_dgrad(dy, lddy, w, dtype, m_offsets, rows, K, N, E, dx, lddx, stream=None):
+    dev, (dy, w, o, dx) = _pointers("moe_grouped_linear_dgrad", (dy, w, m_offsets, dx))
+    return _enqueue((_lib or lib()).moe_grouped_linear_dgrad, dev, stream, dy, lddy, w, dtype, o,
+                    rows, K, N, E, dx, lddx)
+
+
+def moe_grouped_linear_wgrad(dy, lddy, x, ldx, dtype, m_offsets, rows, K, N, E, dw_dtype, dw,
+                             stream=None):
+    dev, (dy, x, o, dw) = _pointers("moe_grouped_linear_wgrad", (dy, x, m_offsets, dw))
+    return _enqueue((_lib or lib()).moe_grouped_linear_wgrad, dev, stream, dy, lddy, x, ldx, dtype,
+                    o, rows, K, N, E, dw_dtype, dw)
+
+
+def moe_lora_workspace_bytes(T, K, R, L, block_m):
+    return int(lib().moe_lora_workspace_bytes(T, K, R, L, block_m))
+
+
+def moe_lora_add(x, ldx, a, b, ranks, scales, dtype, adapter_ids, sorted_token_ids, expert_ids,
+                 num_tokens_post_padded, T, K, N, R, L, block_m, addend, out_dtype, out, ldo,
+                 workspace, stream=None):
+    dev, (x, a, b, r, s, i, st, e, n, c, o, ws) = _pointers(
+        "moe_lora_add", (x, a, b, ranks, scales, adapter_ids, sorted_token_ids, expert_ids,
+                         num_tokens_post_padded, addend, out, workspace))
+    return _enqueue((_lib or lib()).moe_lora_add, dev, stream, x, ldx, a, b, r, s, dtype, i, st, e, n,
+                    T, K, N, R, L, block_m, c, out_dtype, o, ldo, ws)
+
+
+def moe_norm_residual(y, dtype, top_k, residual, r_dtype, w_post, gate, gate_kind, alpha, beta,
+                      w_pre, eps, M, N, r, h, rstd_post, rstd_pre, stream=None):
+    dev, (y, x, wo, g, wr, r, h, fo, fr) = _pointers(
+        "moe_norm_residual", (y, residual, w_post, gate, w_pre, r, h, rstd_post, rstd_pre))
+    return _enqueue((_lib or lib()).moe_norm_residual, dev, stream, y, dtype, top_k, x, r_dtype, wo, g,
+                    gate_kind, alpha, beta, wr, eps, M, N, r, h, fo, fr)
+
+
+def moe_norm_backward_workspace_bytes(M, N):
+    return int(lib().moe_norm_backward_workspace_bytes(M, N))
+
+
+def moe_norm_residual_backward(d_r, d_h, y, dtype, top_k, r, r_dtype, w_post, gate, gate_kind,
+                               alpha, beta, w_pre, rstd_post, rstd_pre, M, N, d_residual, d_y,
+                               d_w_post, d_gate, d_w_pre, workspace, stream=None):
+    dev, (dr, dh, y, r, wo, g, wr, fo, fr, dx, dy, dwo, dg, dwr, ws) = _pointers(
+        "moe_norm_residual_backward", (d_r, d_h, y, r, w_post, gate, w_pre, rstd_post, rstd_pre,
+                                       d_residual, d_y, d_w_post, d_gate, d_w_pre, workspace))
+    return _enqueue((_lib or lib()).moe_norm_residual_backward, dev, stream, dr, dh, y, dtype, top_k,
+                    r, r_dtype, wo, g, gate_kind, alpha, beta, wr, fo, fr, M, N, dx, dy, dwo, dg, dwr,
+                    ws)

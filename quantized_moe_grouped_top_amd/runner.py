@@ -15,25 +15,36 @@ current stream:
     general router : moe_route_topk -> moe_align_topk_ids in place of
                      moe_align_block_size; its gradient moe_route_topk_backward
     dense int8     : moe_quantize_act (int8 per token) -> moe_gemm_int8w8a8, e.g.
-                     a shared expert added to the routed experts' sum
+                     a shared expert added to the routed experts' sum; moe_lora_add
+                     adds the adapters of many requests
+    16-bit experts : moe_gated_up -> moe_grouped_linear; backward
+                     moe_gated_down_backward -> moe_grouped_linear_dgrad and
+                     two moe_grouped_linear_wgrad
+    block's norms  : moe_norm_residual in place of moe_combine; backward
+                     moe_norm_residual_backward
 
 Every step runs in the library's HIP kernels; nothing here computes.
 """
 
 import torch
 
-from . import (MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F16, MOE_F32, MOE_GROUP_MAX,
+from . import (MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F16, MOE_F32, MOE_GATED_GELU,
+               MOE_GATED_SILU, MOE_GATE_CHANNEL, MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GROUP_MAX,
                MOE_GROUP_TOP2, MOE_Q_FP8_PER_CHANNEL, MOE_Q_FP8_PER_TENSOR,
                MOE_Q_INT4_PER_CHANNEL, MOE_Q_INT8_PER_CHANNEL, MOE_Q_MXFP8, MOE_Q_MXFP8_COLWISE,
                MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_FRAG,
                MOE_W_ROWMAJOR,
                MOE_W_TILED, moe_act_quantize, moe_align_block_size, moe_align_max_padded,
-               moe_align_topk_ids, moe_align_workspace_bytes, moe_combine, moe_gemm_int8w8a8,
+               moe_align_topk_ids, moe_align_workspace_bytes, moe_combine, moe_gated_down_backward,
+               moe_gated_up, moe_gemm_int8w8a8,
                moe_gemm_int8w8a8_workspace_bytes,
                moe_grouped_gemm_fp8w8a8, moe_grouped_gemm_fp8w8a16, moe_grouped_gemm_int4w4a16,
                moe_grouped_gemm_int8w8a8,
                moe_grouped_gemm_int8w8a16,
-               moe_grouped_gemm_mxfp8, moe_grouped_gemm_mxfp8_wgrad, moe_quantize_act_colwise,
+               moe_grouped_gemm_mxfp8, moe_grouped_gemm_mxfp8_wgrad, moe_grouped_linear,
+               moe_grouped_linear_dgrad, moe_grouped_linear_wgrad, moe_lora_add,
+               moe_lora_workspace_bytes, moe_norm_backward_workspace_bytes, moe_norm_residual,
+               moe_norm_residual_backward, moe_quantize_act_colwise,
                moe_mx_scale_rows, moe_pack_weights, moe_packed_weight_bytes, moe_quantize_act,
                moe_quantize_weights, moe_quantize_workspace_bytes, moe_recommended_block_m,
                moe_route_topk, moe_route_topk_backward)
@@ -186,9 +197,189 @@ class Int8Linear:
                           self.M, self.K, self.N, self.dtype, out, self.N, self.ws)
         return out
 
-    def forward(self, x, w_q, w_scale, bias=None, addend=None, out=None):
+    def forward(self, x, w_q, w_scale, bias=None, addend=None, out=None, lora=None):
+        """`lora` = (LoraAdapters, a, b, scales, ranks): the adapters' contribution,
+        taken of the unquantized x, is added to the product."""
+        if lora is not None:
+            adapters, a, b, scales, ranks = lora
+            assert adapters.T == self.M and x.dtype == adapters.torch_dtype
+            adapters.check(x, a, b, self.out if out is None else out, scales, ranks)
         self.quantize(x)
-        return self.gemm(w_q, w_scale, bias, addend, out)
+        out = self.gemm(w_q, w_scale, bias, addend, out)
+        if lora is not None:
+            adapters.add(x, a, b, out, out, scales, ranks)
+        return out
+
+
+class LoraAdapters:
+    """Low-rank adapters of many requests beside shared projections: T tokens, L
+    adapters of rank R at most, inputs of K features at most.  `plan` groups the
+    tokens by adapter, once for all projections of a step; `add` adds
+    scales[a] b[a] (a[a] x_t) to a projection's output."""
+
+    def __init__(self, T, K, R, L, dtype="bf16", block_m=None, device="cuda"):
+        self.T, self.K, self.R, self.L = T, K, R, L
+        self.dtype, self.torch_dtype = _DTYPES[dtype]
+        self.block_m = block_m or (16 if T < 2048 else 128)
+        n = moe_align_max_padded(T, L, 1, self.block_m)
+        self.adapter_ids = _empty((T, 1), torch.int32, device)
+        self.sorted_token_ids = _empty((n,), torch.int32, device)
+        self.expert_ids = _empty((n // self.block_m,), torch.int32, device)
+        self.num_tokens_post_padded = _empty((1,), torch.int32, device)
+        self.align_ws = _empty((moe_align_workspace_bytes(T, L, 1),), torch.uint8, device)
+        self.ws = _empty((moe_lora_workspace_bytes(T, K, R, L, self.block_m),), torch.uint8, device)
+
+    def plan(self, adapter_ids):
+        """adapter_ids [T] int32, outside [0, L) for a token without an adapter."""
+        assert adapter_ids.dtype == torch.int32 and adapter_ids.numel() == self.T
+        self.adapter_ids.copy_(adapter_ids.view(self.T, 1))
+        moe_align_topk_ids(self.adapter_ids, self.T, self.L, 1, self.block_m, 0,
+                           self.sorted_token_ids, self.expert_ids, self.num_tokens_post_padded,
+                           None, self.align_ws)
+
+    def check(self, x, a, b, out, scales=None, ranks=None):
+        K, N = a.shape[2], b.shape[1]
+        assert x.dtype == self.torch_dtype and tuple(x.shape) == (self.T, K) and K <= self.K
+        assert x.stride(1) == 1
+        assert _rows_of(a, self.torch_dtype, (self.L, self.R, K))
+        assert _rows_of(b, self.torch_dtype, (self.L, N, self.R))
+        assert tuple(out.shape) == (self.T, N) and out.stride(1) == 1
+        assert scales is None or _rows_of(scales, torch.float32, (self.L,))
+        assert ranks is None or _rows_of(ranks, torch.int32, (self.L,))
+
+    def add(self, x, a, b, out, addend=None, scales=None, ranks=None):
+        """out = addend + the adapters' part; `addend` may be out (or None: 0)."""
+        self.check(x, a, b, out, scales, ranks)
+        assert addend is None or (addend.dtype == out.dtype and addend.shape == out.shape and
+                                  addend.stride() == out.stride())
+        code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[out.dtype]
+        # a workspace for K features holds that of fewer
+        K, N = a.shape[2], b.shape[1]
+        moe_lora_add(x, x.stride(0), a, b, ranks, scales, self.dtype, self.adapter_ids,
+                     self.sorted_token_ids, self.expert_ids, self.num_tokens_post_padded, self.T, K,
+                     N, self.R, self.L, self.block_m, addend, code, out, out.stride(0), self.ws)
+        return out
+
+
+class GatedFFN:
+    """Gated feed-forward of E experts in 16 bits over expert-concatenated rows:
+    x [rows, K] -> y [rows, K] through w_up [E, 2H, K] (gate, then up) and w_down
+    [E, K, H].  With `train` the forward pass keeps what `backward` reads."""
+
+    def __init__(self, rows, K, H, E, dtype="bf16", act="silu", train=False, dw="same",
+                 device="cuda"):
+        self.rows, self.K, self.H, self.E = rows, K, H, E
+        self.dtype, self.torch_dtype = _DTYPES[dtype]
+        assert self.dtype != MOE_F32
+        self.act = {"silu": MOE_GATED_SILU, "gelu": MOE_GATED_GELU}[act]
+        t = self.torch_dtype
+        self.h = _empty((rows, H), t, device)
+        self.y = _empty((rows, K), t, device)
+        self.gu = None
+        if train:
+            self.dw_dtype, dw_t = (MOE_F32, torch.float32) if dw == "f32" else (self.dtype, t)
+            self.gu = _empty((rows, 2 * H), t, device)
+            self.dgu = _empty((rows, 2 * H), t, device)
+            self.dx = _empty((rows, K), t, device)
+            self.dw_up = _empty((E, 2 * H, K), dw_t, device)
+            self.dw_down = _empty((E, K, H), dw_t, device)
+
+    def _check(self, x, w_up, w_down, m_offsets):
+        t = self.torch_dtype
+        assert x.dtype == t and tuple(x.shape) == (self.rows, self.K) and x.stride(1) == 1
+        assert _rows_of(w_up, t, (self.E, 2 * self.H, self.K))
+        assert _rows_of(w_down, t, (self.E, self.K, self.H))
+        assert m_offsets is None or _rows_of(m_offsets, torch.int32, (self.E + 1,))
+
+    def forward(self, x, w_up, w_down, m_offsets=None):
+        self._check(x, w_up, w_down, m_offsets)
+        moe_gated_up(x, x.stride(0), w_up, self.dtype, m_offsets, self.rows, self.K, self.H, self.E,
+                     self.act, self.gu, self.h)
+        moe_grouped_linear(self.h, self.H, w_down, self.dtype, m_offsets, self.rows, self.H, self.K,
+                           self.E, self.y, self.K)
+        return self.y
+
+    def backward(self, dy, x, w_up, w_down, m_offsets=None):
+        """(dx, dw_up, dw_down) of the forward pass before."""
+        self._check(x, w_up, w_down, m_offsets)
+        assert self.gu is not None, "GatedFFN(train=True) keeps what the gradient needs"
+        assert dy.dtype == self.torch_dtype and tuple(dy.shape) == (self.rows, self.K)
+        assert dy.stride(1) == 1
+        rows, K, H, E, t = self.rows, self.K, self.H, self.E, self.dtype
+        # h is there from the forward pass
+        moe_gated_down_backward(dy, dy.stride(0), w_down, self.gu, t, m_offsets, rows, K, H, E,
+                                self.act, self.dgu, None)
+        moe_grouped_linear_dgrad(self.dgu, 2 * H, w_up, t, m_offsets, rows, K, 2 * H, E, self.dx, K)
+        moe_grouped_linear_wgrad(self.dgu, 2 * H, x, x.stride(0), t, m_offsets, rows, K, 2 * H, E,
+                                 self.dw_dtype, self.dw_up)
+        moe_grouped_linear_wgrad(dy, dy.stride(0), self.h, H, t, m_offsets, rows, H, K, E,
+                                 self.dw_dtype, self.dw_down)
+        return self.dx, self.dw_up, self.dw_down
+
+
+class BlockNorm:
+    """What follows a block and precedes the next, for M tokens of N features:
+    combine of the top_k slots, norm after the block, gate, residual, next norm."""
+
+    def __init__(self, M, N, top_k=1, dtype="bf16", r_dtype=None, gate="none", alpha=1.0, beta=1.0,
+                 eps=1e-6, train=False, device="cuda"):
+        self.M, self.N, self.top_k = M, N, top_k
+        self.dtype, self.torch_dtype = _DTYPES[dtype]
+        self.r_dtype, self.r_torch_dtype = _DTYPES[r_dtype or dtype]
+        self.gate_kind = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL,
+                          "token": MOE_GATE_TOKEN}[gate]
+        self.gate_size = {"none": None, "channel": (N,), "token": (M,)}[gate]
+        self.alpha, self.beta, self.eps = alpha, beta, eps
+        self.r = _empty((M, N), self.r_torch_dtype, device)
+        self.h = _empty((M, N), self.torch_dtype, device)
+        self.rstd_post = self.rstd_pre = None
+        if train:
+            self.rstd_post = _empty((M,), torch.float32, device)
+            self.rstd_pre = _empty((M,), torch.float32, device)
+            self.d_residual = _empty((M, N), self.r_torch_dtype, device)
+            self.d_y = _empty((M, N), self.torch_dtype, device)
+            self.d_w_post = _empty((N,), torch.float32, device)
+            self.d_w_pre = _empty((N,), torch.float32, device)
+            self.d_gate = _empty(self.gate_size or (0,), torch.float32, device)
+            self.ws = _empty((moe_norm_backward_workspace_bytes(M, N),), torch.uint8, device)
+
+    def check(self, y, residual, w_pre, w_post, gate):
+        M, N = self.M, self.N
+        # the grouped GEMMs leave the bits of bf16 values as int16
+        assert y is None or _rows_of(y, self.torch_dtype, (M * self.top_k, N)) or (
+            self.dtype == MOE_BF16 and _rows_of(y, torch.int16, (M * self.top_k, N)))
+        assert residual is None or _rows_of(residual, self.r_torch_dtype, (M, N))
+        for w in (w_pre, w_post):
+            assert w is None or _rows_of(w, torch.float32, (N,))
+        assert (gate is None) == (self.gate_size is None)
+        assert gate is None or _rows_of(gate, torch.float32, self.gate_size)
+
+    def forward(self, y, residual, w_pre=None, w_post=None, gate=None):
+        """(r, h): the new residual and, with w_pre, the next block's input."""
+        self.check(y, residual, w_pre, w_post, gate)
+        h = None if w_pre is None else self.h
+        moe_norm_residual(y, self.dtype, self.top_k, residual, self.r_dtype, w_post, gate,
+                          self.gate_kind, self.alpha, self.beta, w_pre, self.eps, self.M, self.N,
+                          self.r, h, None if w_post is None else self.rstd_post,
+                          None if w_pre is None else self.rstd_pre)
+        return self.r, h
+
+    def backward(self, d_r, d_h, y, w_pre=None, w_post=None, gate=None):
+        """(d_residual, d_y, d_w_pre, d_w_post, d_gate) of the forward pass before,
+        None for what it did not have; d_y [M, N] is the gradient of each slot."""
+        self.check(y, None, w_pre, w_post, gate)
+        assert self.rstd_pre is not None, "BlockNorm(train=True) keeps what the gradient needs"
+        assert d_r is None or _rows_of(d_r, self.r_torch_dtype, (self.M, self.N))
+        assert d_h is None or _rows_of(d_h, self.torch_dtype, (self.M, self.N))
+        d_y = None if y is None else self.d_y
+        d_w_pre = None if w_pre is None else self.d_w_pre
+        d_w_post = None if w_post is None else self.d_w_post
+        d_gate = None if gate is None else self.d_gate
+        moe_norm_residual_backward(d_r, d_h, y, self.dtype, self.top_k, self.r, self.r_dtype, w_post,
+                                   gate, self.gate_kind, self.alpha, self.beta, w_pre,
+                                   self.rstd_post, self.rstd_pre, self.M, self.N, self.d_residual,
+                                   d_y, d_w_post, d_gate, d_w_pre, self.ws)
+        return self.d_residual, d_y, d_w_pre, d_w_post, d_gate
 
 
 class RoutedMoE:
@@ -280,11 +471,19 @@ class RoutedMoE:
     def combine(self):
         moe_combine(self.y, self.M, self.N, self.top_k, self.out)
 
-    def forward(self, x, logits, w_q, w_scale, bias=None, shared=None):
+    def forward(self, x, logits, w_q, w_scale, bias=None, shared=None, norm=None):
         """One pass of the hot path; returns the bf16 output bits [M, N] (int16).
         `bias`: the router's balance bias; `shared` = (Int8Linear, w_q, w_scale):
         a shared expert of the layer's M, K and N whose product is added to the
-        routed experts' sum."""
+        routed experts' sum.  `norm` = (BlockNorm, residual, w_pre, w_post, gate):
+        the norm after the layer, gate, residual and next norm, and their (r, h) is
+        returned; without a shared expert (top_k of the BlockNorm that of the layer)
+        it takes the place of the combine, with one (top_k 1) it follows the sum."""
+        if norm is not None:
+            block, norm_args = norm[0], norm[1:]
+            assert (block.M, block.N, block.dtype) == (self.M, self.N, MOE_BF16)
+            assert block.top_k == (1 if shared is not None else self.top_k)
+            block.check(self.out if shared is not None else self.y, *norm_args)
         if shared is not None:
             linear = shared[0]
             assert (linear.M, linear.K, linear.N) == (self.M, self.K, self.N)
@@ -292,11 +491,13 @@ class RoutedMoE:
         self.route(logits, bias)
         self.quantize(x)
         self.gemm(x, w_q, w_scale)
+        if norm is not None and shared is None:
+            return block.forward(self.y, *norm_args)
         self.combine()
         if shared is not None:
             linear, sh_q, sh_scale = shared
             linear.forward(x, sh_q, sh_scale, addend=self.out, out=self.out)
-        return self.out
+        return self.out if norm is None else block.forward(self.out, *norm_args)
 
 
 class MxMoE:

@@ -1,0 +1,312 @@
+"""The operators of the block around the experts without a GPU: exports, sizes,
+every refusal (before anything is enqueued), and the float64 reference they are
+tested against: closed forms and central differences."""
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+
+import quantized_moe_grouped_top_amd as qm
+from oracle import block as B
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe_block.h")
+FAKE = 1 << 20
+INV, UNS = qm.MOE_EINVAL, qm.MOE_EUNSUPPORTED
+
+
+def _gpu_visible():
+    import torch
+    return torch.cuda.is_available()
+
+
+needs_lib = pytest.mark.skipif(not os.path.exists(qm.LIB_PATH), reason="libqmoe.so not built")
+no_gpu = pytest.mark.skipif(_gpu_visible(), reason="fake-pointer error paths run only without a GPU")
+
+
+@needs_lib
+def test_block_symbols_and_constants():
+    raw = open(HEADER).read()
+    text = re.sub(r"/\*.*?\*/", "", raw, flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
+    assert names == sorted(qm.BLOCK_EXPORTS)
+    h = ctypes.CDLL(qm.LIB_PATH)
+    for n in names:
+        assert hasattr(h, n), n
+    for name, value in re.findall(r"#define (MOE_[A-Z0-9_]+)\s+(\(1 << \d+\)|\d+)", text):
+        assert getattr(qm, name) == eval(value), name
+
+
+@needs_lib
+def test_workspace_sizes():
+    """LoRA: a float32 for every sorted slot, rank and share of K (8 shares of 512 k at
+    least); norms: three rows of N for each of 512 workgroups at most."""
+    for T, K, R, L, b in [(1, 4096, 16, 8, 16), (64, 4096, 64, 32, 16), (4096, 4096, 64, 8, 128),
+                          (65536, 64, 128, 128, 256), (1, 8, 8, 1, 16)]:
+        n = qm.moe_lora_workspace_bytes(T, K, R, L, b)
+        one = qm.moe_align_max_padded(T, L, 1, b) * R * 4
+        assert n % one == 0 and 1 <= n // one <= min(8, max(1, K // 512)), (T, K, R, L, b)
+        assert qm.moe_lora_workspace_bytes(T, 2 * K, R, L, b) >= n    # a larger K holds a smaller
+    for bad in [(0, 64, 8, 1, 16), (1, 63, 8, 1, 16), (1, 64, 4, 1, 16), (1, 64, 136, 1, 16),
+                (1, 64, 8, 129, 16), (1, 64, 8, 0, 16), (65537, 64, 8, 1, 16), (1, 64, 8, 1, 8)]:
+        assert qm.moe_lora_workspace_bytes(*bad) == 0
+    for M, N in [(1, 8), (100, 4096), (8192, 6144), (1 << 24, 8)]:
+        n = qm.moe_norm_backward_workspace_bytes(M, N)
+        assert n > 0 and n % (3 * N * 4) == 0 and n <= 3 * 512 * N * 4
+    for bad in [(0, 8), (4, 12), (4, 16392), ((1 << 24) + 1, 8)]:
+        assert qm.moe_norm_backward_workspace_bytes(*bad) == 0
+
+
+def _refused(call, kw, code, name):
+    with pytest.raises(qm.MoeError) as ei:
+        call(**kw)
+    assert ei.value.code == code and name in str(ei.value)
+
+
+GROUPED = [
+    (dict(dtype=0), INV), (dict(dtype=3), INV), (dict(rows=-1), INV), (dict(E=0), INV),
+    (dict(E=129), UNS), (dict(rows=(1 << 24) + 1), UNS), (dict(m_offsets=None), INV),
+    (dict(m_offsets=FAKE + 2), INV),
+]
+
+
+def _case(kw, **base):
+    base.update(kw)
+    return base
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", GROUPED + [
+    (dict(act=2), INV), (dict(K=0), INV), (dict(K=60), UNS), (dict(H=60), UNS),
+    (dict(K=(1 << 20) + 8, ldx=(1 << 20) + 8), UNS), (dict(H=(1 << 19) + 8), UNS),
+    (dict(ldx=56), INV), (dict(ldx=68), UNS), (dict(ldx=(1 << 20) + 8), UNS), (dict(x=None), INV),
+    (dict(w=None), INV), (dict(h=None), INV), (dict(x=FAKE + 8), INV), (dict(w=FAKE + 8), INV),
+    (dict(gu=FAKE + 8), INV), (dict(h=FAKE + 8), INV),
+])
+def test_gated_up_rejects(kw, code):
+    _refused(qm.moe_gated_up, _case(kw, x=FAKE, ldx=64, w=FAKE, dtype=1, m_offsets=FAKE, rows=16,
+                                    K=64, H=64, E=4, act=0, gu=FAKE, h=FAKE, stream=0), code,
+             "moe_gated_up")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", GROUPED + [
+    (dict(K=4), UNS), (dict(N=0), INV), (dict(N=12), UNS), (dict(ldx=56), INV), (dict(ldy=56), INV),
+    (dict(ldy=70), UNS), (dict(x=None), INV), (dict(w=None), INV), (dict(y=None), INV),
+    (dict(y=FAKE + 4), INV),
+])
+def test_grouped_linear_rejects(kw, code):
+    _refused(qm.moe_grouped_linear, _case(kw, x=FAKE, ldx=64, w=FAKE, dtype=2, m_offsets=FAKE,
+                                          rows=16, K=64, N=64, E=4, y=FAKE, ldy=64, stream=0), code,
+             "moe_grouped_linear")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", GROUPED + [
+    (dict(act=-1), INV), (dict(N=4), UNS), (dict(H=4), UNS), (dict(lddy=56), INV),
+    (dict(dy=None), INV), (dict(w=None), INV), (dict(gu=None), INV), (dict(dgu=None), INV),
+    (dict(dgu=FAKE + 8), INV), (dict(h=FAKE + 8), INV),
+])
+def test_gated_down_backward_rejects(kw, code):
+    _refused(qm.moe_gated_down_backward,
+             _case(kw, dy=FAKE, lddy=64, w=FAKE, gu=FAKE, dtype=1, m_offsets=FAKE, rows=16, N=64,
+                   H=64, E=4, act=0, dgu=FAKE, h=None, stream=0), code, "moe_gated_down_backward")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", GROUPED + [
+    (dict(K=4), UNS), (dict(N=4), UNS), (dict(lddy=56), INV), (dict(lddx=56), INV),
+    (dict(dy=None), INV), (dict(w=None), INV), (dict(dx=None), INV), (dict(dx=FAKE + 2), INV),
+])
+def test_dgrad_rejects(kw, code):
+    _refused(qm.moe_grouped_linear_dgrad,
+             _case(kw, dy=FAKE, lddy=64, w=FAKE, dtype=1, m_offsets=FAKE, rows=16, K=64, N=64, E=4,
+                   dx=FAKE, lddx=64, stream=0), code, "moe_grouped_linear_dgrad")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", GROUPED + [
+    (dict(K=4), UNS), (dict(N=4), UNS), (dict(lddy=56), INV), (dict(ldx=56), INV),
+    (dict(dw_dtype=2), INV), (dict(dy=None), INV), (dict(x=None), INV), (dict(dw=None), INV),
+    (dict(dw=None, rows=0), INV), (dict(dw=FAKE + 4), INV),
+])
+def test_wgrad_rejects(kw, code):
+    _refused(qm.moe_grouped_linear_wgrad,
+             _case(kw, dy=FAKE, lddy=64, x=FAKE, ldx=64, dtype=1, m_offsets=FAKE, rows=16, K=64,
+                   N=64, E=4, dw_dtype=0, dw=FAKE, stream=0), code, "moe_grouped_linear_wgrad")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=0), INV), (dict(out_dtype=3), INV), (dict(T=-1), INV), (dict(T=65537), UNS),
+    (dict(L=0), INV), (dict(L=129), UNS), (dict(block_m=8), UNS), (dict(R=0), INV), (dict(R=12), UNS),
+    (dict(R=136), UNS), (dict(K=0), INV), (dict(K=12), UNS), (dict(N=12), UNS), (dict(ldx=56), INV),
+    (dict(ldo=56), INV), (dict(ldo=68), UNS), (dict(x=None), INV), (dict(a=None), INV),
+    (dict(b=None), INV), (dict(sorted_token_ids=None), INV), (dict(expert_ids=None), INV),
+    (dict(num_tokens_post_padded=None), INV), (dict(out=None), INV), (dict(workspace=None), INV),
+    (dict(adapter_ids=None), INV), (dict(adapter_ids=None, addend=None), INV),
+    (dict(workspace=FAKE + 4), INV), (dict(ranks=FAKE + 1), INV), (dict(scales=FAKE + 2), INV),
+    (dict(addend=FAKE + 8), INV), (dict(b=FAKE + 8), INV),
+])
+def test_lora_rejects(kw, code):
+    _refused(qm.moe_lora_add,
+             _case(kw, x=FAKE, ldx=64, a=FAKE, b=FAKE, ranks=FAKE, scales=FAKE, dtype=1,
+                   adapter_ids=FAKE, sorted_token_ids=FAKE, expert_ids=FAKE,
+                   num_tokens_post_padded=FAKE, T=16, K=64, N=64, R=16, L=4, block_m=16,
+                   addend=2 * FAKE, out_dtype=1, out=FAKE, ldo=64, workspace=FAKE, stream=0), code,
+             "moe_lora_add")
+
+
+NORM = [
+    (dict(dtype=0), INV), (dict(r_dtype=2), INV), (dict(M=-1), INV), (dict(N=0), INV),
+    (dict(N=12), UNS), (dict(N=16392), UNS), (dict(top_k=0), INV), (dict(top_k=9), UNS),
+    (dict(M=1 << 23, top_k=3), UNS), (dict(gate_kind=3), INV), (dict(gate_kind=0), INV),
+    (dict(gate=None), INV), (dict(gate=FAKE + 4), INV), (dict(gate_kind=2, gate=FAKE + 2), INV),
+    (dict(y=FAKE + 8), INV),
+]
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", NORM + [
+    (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV), (dict(y=None), INV),
+    (dict(y=None, gate=None, gate_kind=0), INV),
+    (dict(y=None, gate=None, gate_kind=0, w_post=None, rstd_post=None, residual=None), INV),
+    (dict(w_pre=None), INV), (dict(h=None), INV), (dict(w_post=None), INV),
+    (dict(w_pre=None, h=None), INV), (dict(r=None), INV), (dict(r=FAKE + 4), INV),
+    (dict(w_pre=FAKE + 4), INV), (dict(h=FAKE + 4), INV), (dict(residual=FAKE + 8), INV),
+    (dict(rstd_pre=FAKE + 2), INV),
+])
+def test_norm_rejects(kw, code):
+    _refused(qm.moe_norm_residual,
+             _case(kw, y=FAKE, dtype=1, top_k=2, residual=FAKE, r_dtype=0, w_post=FAKE, gate=FAKE,
+                   gate_kind=1, alpha=1.0, beta=1.0, w_pre=FAKE, eps=1e-6, M=16, N=64, r=FAKE,
+                   h=FAKE, rstd_post=FAKE, rstd_pre=FAKE, stream=0), code, "moe_norm_residual")
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("kw,code", NORM + [
+    (dict(d_h=None), INV), (dict(w_pre=None), INV),
+    (dict(d_h=None, w_pre=None, d_w_pre=None, d_r=None), INV), (dict(d_y=None), INV),
+    (dict(y=None), INV), (dict(w_post=None), INV), (dict(gate=None, gate_kind=0), INV),
+    (dict(rstd_post=None), INV), (dict(rstd_pre=None), INV), (dict(r=None), INV),
+    (dict(workspace=None), INV), (dict(workspace=FAKE + 8), INV), (dict(d_y=FAKE + 8), INV),
+    (dict(d_residual=FAKE + 8), INV), (dict(d_gate=FAKE + 2), INV),
+])
+def test_norm_backward_rejects(kw, code):
+    _refused(qm.moe_norm_residual_backward,
+             _case(kw, d_r=FAKE, d_h=FAKE, y=FAKE, dtype=1, top_k=2, r=FAKE, r_dtype=0, w_post=FAKE,
+                   gate=FAKE, gate_kind=1, alpha=1.0, beta=1.0, w_pre=FAKE, rstd_post=FAKE,
+                   rstd_pre=FAKE, M=16, N=64, d_residual=FAKE, d_y=FAKE, d_w_post=FAKE, d_gate=FAKE,
+                   d_w_pre=FAKE, workspace=FAKE, stream=0), code, "moe_norm_residual_backward")
+
+
+@needs_lib
+def test_host_tensors_are_refused():
+    import torch
+    x = torch.zeros(16, 64, dtype=torch.bfloat16)
+    with pytest.raises(qm.MoeError):
+        qm.moe_grouped_linear(x, 64, x, 1, None, 16, 64, 16, 1, x, 64)
+
+
+# ---- the reference ------------------------------------------------------------------
+def test_activations():
+    g = np.linspace(-12, 12, 97)
+    for kind in (B.SILU, B.GELU):
+        a, da = B.act(g, kind)
+        d = 1e-6
+        np.testing.assert_allclose(da, (B.act(g + d, kind)[0] - B.act(g - d, kind)[0]) / (2 * d),
+                                   atol=1e-8)
+        assert abs(a[48]) == 0 and a[-1] == pytest.approx(12.0, rel=1e-4) and abs(a[0]) < 1e-4
+
+
+def _numeric(f, v, d=1e-6):
+    """Central differences of the scalar f with respect to every element of v."""
+    out = np.zeros_like(v)
+    for i in np.ndindex(v.shape):
+        keep = v[i]
+        v[i] = keep + d
+        hi = f()
+        v[i] = keep - d
+        out[i] = (hi - f()) / (2 * d)
+        v[i] = keep
+    return out
+
+
+@pytest.mark.parametrize("kind", [B.SILU, B.GELU])
+def test_feed_forward_gradients_by_differences(kind):
+    rng = np.random.default_rng(3 + kind)
+    rows, K, H, E = 7, 4, 3, 3
+    segs = B.segments([0, 4, 4, 6], rows)                 # expert 1 and row 6 left out
+    x, w_up, w_down = (rng.normal(size=s) for s in [(rows, K), (E, 2 * H, K), (E, K, H)])
+    dy = rng.normal(size=(rows, K))
+
+    def forward():
+        gu, h = B.gated_up(x, w_up, segs, kind, np.zeros((rows, 2 * H)), np.zeros((rows, H)))
+        return gu, h, B.grouped_linear(h, w_down, segs, np.zeros((rows, K)))
+
+    def loss():
+        return float((forward()[2] * dy).sum())
+
+    gu, h, _ = forward()
+    dgu, h2 = B.gated_down_backward(dy, w_down, gu, segs, kind, np.zeros_like(gu), np.zeros_like(h))
+    np.testing.assert_allclose(h2, h, atol=1e-14)
+    np.testing.assert_allclose(B.grouped_dgrad(dgu, w_up, segs, np.zeros_like(x)), _numeric(loss, x),
+                               atol=1e-7)
+    np.testing.assert_allclose(B.grouped_wgrad(dgu, x, segs), _numeric(loss, w_up), atol=1e-7)
+    np.testing.assert_allclose(B.grouped_wgrad(dy, h, segs), _numeric(loss, w_down), atol=1e-7)
+
+
+@pytest.mark.parametrize("kind", [B.GATE_NONE, B.GATE_CHANNEL, B.GATE_TOKEN])
+@pytest.mark.parametrize("post", [False, True])
+def test_norm_gradients_by_differences(kind, post):
+    rng = np.random.default_rng(17 + kind)
+    M, N, k, eps = 3, 5, 2, 1e-3
+    y, x = rng.normal(size=(M * k, N)), rng.normal(size=(M, N))
+    w_post = rng.normal(size=N) if post else None
+    w_pre = rng.normal(size=N)
+    gate = [None, rng.normal(size=N), rng.normal(size=M)][kind]
+    d_r, d_h = rng.normal(size=(M, N)), rng.normal(size=(M, N))
+
+    def forward():
+        return B.norm_residual(y, k, x, w_post, gate, kind, 0.8, 0.6, w_pre, eps, M, N)
+
+    def loss():
+        r, h, _, _ = forward()
+        return float((r * d_r).sum() + (h * d_h).sum())
+
+    r, _, f_post, f_pre = forward()
+    dx, dy, dwo, dg, dwr = B.norm_residual_backward(d_r, d_h, y, k, r, w_post, gate, kind, 0.8, 0.6,
+                                                    w_pre, f_post, f_pre, M, N)
+    np.testing.assert_allclose(dx, _numeric(loss, x), atol=1e-7)
+    np.testing.assert_allclose(np.repeat(dy, k, axis=0), _numeric(loss, y), atol=1e-7)
+    np.testing.assert_allclose(dwr, _numeric(loss, w_pre), atol=1e-7)
+    if post:
+        np.testing.assert_allclose(dwo, _numeric(loss, w_post), atol=1e-7)
+    if kind:
+        np.testing.assert_allclose(dg, _numeric(loss, gate), atol=1e-7)
+
+
+def test_lora_reference_is_the_merged_weight():
+    rng = np.random.default_rng(5)
+    T, K, N, R, L = 6, 5, 4, 3, 2
+    x, a, b = rng.normal(size=(T, K)), rng.normal(size=(L, R, K)), rng.normal(size=(L, N, R))
+    a[1, 2:] = np.nan                                      # past adapter 1's rank
+    b[1, :, 2:] = np.nan
+    ids, ranks, scales = [0, 1, -1, 1, 2, 0], [3, 2], np.array([0.5, 2.0])
+    add = rng.normal(size=(T, N))
+    out = B.lora(x, a, b, ids, ranks, scales, add)
+    merged = [0.5 * b[0] @ a[0], 2.0 * b[1, :, :2] @ a[1, :2]]
+    for t, i in enumerate(ids):
+        want = add[t] + (merged[i] @ x[t] if 0 <= i < L else 0.0)
+        np.testing.assert_allclose(out[t], want, atol=1e-12)

@@ -1,0 +1,162 @@
+"""The operators of the block around the experts as they run together: a routed
+layer between its norms, an adapter beside a dense projection, the 16-bit experts
+of a training step; on other streams, two at a time and in replayed graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_grouped_top_amd as qm
+from oracle import block as B
+from quantized_moe_grouped_top_amd import runner
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+M, K, E, K2 = 48, 256, 8, 2
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _layer(shared):
+    """norm -> router and experts (-> shared expert with an adapter) -> norm"""
+    g = _gen(11)
+    rnd = lambda *s, d=torch.float32, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(d)  # noqa: E731
+    bf = torch.bfloat16
+    first, last = runner.BlockNorm(M, K), runner.BlockNorm(M, K, 1 if shared else K2, gate="token",
+                                                           beta=0.5)
+    router = runner.TopKRouter(M, E, K2)
+    moe = runner.RoutedMoE("int8dq", M, K, K, E, K2, router=router)
+    w_q, w_s = runner.quantize_weights(rnd(E, K, K, m=K ** -0.5), "int8dq")
+    sh_q, sh_s = runner.quantize_weights(rnd(1, K, K, m=K ** -0.5), "int8")
+    lin = runner.Int8Linear(M, K, K)
+    w_pre, w_next, w_post = (1.0 + rnd(K, m=0.1) for _ in range(3))
+    gate, w_gate, x = rnd(M).abs(), rnd(K, E, m=K ** -0.5), rnd(M, K, d=bf)
+
+    def run():
+        r, h = first.forward(None, x, w_pre)
+        logits = h.float() @ w_gate
+        sh = (lin, sh_q[0], sh_s[0]) if shared else None
+        return moe.forward(h, logits, w_q, w_s, shared=sh, norm=(last, r, w_next, w_post, gate))
+
+    return run, moe, first, last, (x, w_pre, w_next, w_post, gate)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_layer_between_its_norms(shared):
+    run, moe, first, last, (x, w_pre, w_next, w_post, gate) = _layer(shared)
+    r, h = run()
+    n = lambda t: t.double().cpu().numpy()                                           # noqa: E731
+    y = moe.out if shared else moe.y
+    slots = n(y.view(torch.bfloat16))
+    rr, rh, _, _ = B.norm_residual(slots, 1 if shared else K2, n(first.r), n(w_post), n(gate),
+                                   B.GATE_TOKEN, 1.0, 0.5, n(w_next), 1e-6, M, K)
+    # bf16 half a step and 2^-16 for the float32 work
+    for got, ref in ((r, rr), (h, rh)):
+        assert np.all(np.abs(n(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -14)
+    assert torch.equal(first.r, x)                        # alpha = 1, no block: the residual itself
+    if not shared:                                        # the combine, then the same from its sums
+        moe.combine()
+        one = runner.BlockNorm(M, K, 1, gate="token", beta=0.5)
+        r2, _ = one.forward(moe.out, first.r, w_next, w_post, gate)
+        assert float((r2.float() - r.float()).abs().max()) < 0.1
+
+
+def _training():
+    g = _gen(5)
+    splits, Kd, H = [70, 0, 33, 150], 136, 264
+    rows = sum(splits)
+    off = torch.tensor(np.cumsum([0] + splits), dtype=torch.int32, device=DEV)
+    rnd = lambda *s, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    ffn = runner.GatedFFN(rows, Kd, H, 4, train=True)
+    norm = runner.BlockNorm(rows, Kd, 1, gate="channel", train=True)
+    x, res, d_r, d_h = (rnd(rows, Kd) for _ in range(4))
+    w_up, w_down = rnd(4, 2 * H, Kd, m=Kd ** -0.5), rnd(4, Kd, H, m=H ** -0.5)
+    w1, w2, gate = (torch.rand(Kd, generator=g, device=DEV) + 0.5 for _ in range(3))
+
+    def run():
+        y = ffn.forward(x, w_up, w_down, off)
+        r, h = norm.forward(y, res, w1, w2, gate)
+        grads = norm.backward(d_r, d_h, y, w1, w2, gate)
+        return (y, r, h) + grads + ffn.backward(grads[1], x, w_up, w_down, off)
+
+    return run, (x, res, d_r, d_h)
+
+
+def _adapters():
+    g = _gen(7)
+    T, Kd, N, R, L = 40, 264, 136, 32, 5
+    rnd = lambda *s, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    ad = runner.LoraAdapters(T, Kd, R, L)
+    ids = torch.randint(-1, L, (T,), generator=g, device=DEV, dtype=torch.int32)
+    x, a, b, add = rnd(T, Kd), rnd(L, R, Kd, m=Kd ** -0.5), rnd(L, N, R), rnd(T, N)
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+
+    def run():
+        ad.plan(ids)
+        return (ad.add(x, a, b, out, add),)
+
+    return run, (x, add)
+
+
+JOBS = {"training": _training, "adapters": _adapters,
+        "layer": lambda: (lambda v: (v[0], (v[4][0],)))(_layer(True))}
+
+
+@pytest.mark.parametrize("name", sorted(JOBS))
+def test_graph_replays(name):
+    """Captured once, replayed with new inputs in the same buffers, eager runs between."""
+    run, inputs = JOBS[name]()
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        run()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            outs = run()
+    for turn in range(4):
+        for i, t in enumerate(inputs):
+            t.copy_(torch.randn(t.shape, generator=_gen(100 * turn + i), device=DEV))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs if t is not None]
+        want = [t.clone() for t in run() if t is not None]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+        assert all(bool(torch.isfinite(t.float()).all()) for t in got if t.dtype != torch.int16)
+
+
+def test_two_streams_at_once():
+    """Two of each job on streams of their own give what each gives alone."""
+    jobs = [JOBS[n]()[0] for n in sorted(JOBS) for _ in range(2)]
+    alone = []
+    for run in jobs:
+        alone.append([t.clone() for t in run() if t is not None])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = []
+    for s, run in zip(streams, jobs):
+        with torch.cuda.stream(s):
+            outs.append(run())
+    torch.cuda.synchronize()
+    for want, got in zip(alone, outs):
+        assert all(torch.equal(a, b) for a, b in zip(want, [t for t in got if t is not None]))
+
+
+def test_named_stream_is_the_one_that_runs():
+    """The stream given by hand, not the current one."""
+    x = torch.randn(64, 512, device=DEV).to(torch.bfloat16)
+    r, ref = torch.zeros_like(x), torch.zeros_like(x)
+    w = torch.ones(512, device=DEV)
+    h = torch.zeros_like(x)
+    qm.moe_norm_residual(None, 1, 1, x, 1, None, None, 0, 2.0, 1.0, w, 1e-6, 64, 512, ref, h, None, None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    qm.moe_norm_residual(None, 1, 1, x, 1, None, None, 0, 2.0, 1.0, w, 1e-6, 64, 512, r, h, None, None,
+                         stream=s)
+    s.synchronize()
+    assert torch.equal(r, ref) and torch.equal(r, (2 * x.float()).to(torch.bfloat16))

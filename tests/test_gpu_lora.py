@@ -1,0 +1,191 @@
+"""Low-rank adapters of many requests on the GPU against the float64 reference.
+
+Tolerance.  v = A x: K products summed in float32 (K * 2^-23 of the magnitudes);
+its two 16-bit parts leave out 2^-16 of v, and in fp16 2^-24 of the token's largest
+value besides; B v: 2 R products summed in float32; the addend's sum and the scale
+round once each; half a step of the output's type."""
+
+import zlib
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_grouped_top_amd as qm
+from oracle import block as B
+from quantized_moe_grouped_top_amd import runner
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f32": (0, torch.float32), "bf16": (1, torch.bfloat16), "f16": (2, torch.float16)}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -24}
+U = 2.0 ** -23
+
+
+def _rng(*what):
+    return torch.Generator().manual_seed(zlib.crc32(repr(what).encode()) & 0x7FFFFFFF)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+class Case:
+    def __init__(self, T, K, N, R, L, dtype, out, block_m, ids, ranks=True, scales=True, std=1.0):
+        g = _rng(T, K, N, R, L, dtype, out, block_m)
+        t = DT[dtype][1]
+        self.T, self.K, self.N, self.R, self.L, self.dtype, self.out = T, K, N, R, L, dtype, out
+        if ids == "random":
+            self.ids = torch.randint(-1, L + 1, (T,), generator=g, dtype=torch.int32)
+        elif ids == "runs":
+            self.ids = (torch.arange(T) * L // T).int()
+        else:
+            self.ids = torch.full((T,), ids, dtype=torch.int32)
+        self.x = torch.full((T, K + 8), float("nan"), dtype=t)
+        self.x[:, :K] = (torch.randn(T, K, generator=g) * std).to(t)
+        self.a = (torch.randn(L, R, K, generator=g) * K ** -0.5).to(t)
+        self.b = (torch.randn(L, N, R, generator=g) * R ** -0.5).to(t)
+        self.ranks = None
+        if ranks:                                # what lies past a rank is never used
+            self.ranks = torch.randint(0, R + 1, (L,), generator=g, dtype=torch.int32)
+            for i, r in enumerate(self.ranks.tolist()):
+                self.a[i, r:] = float("nan")
+                self.b[i, :, r:] = float("nan")
+        self.scales = torch.rand(L, generator=g) + 0.5 if scales else None
+        self.add = torch.randn(T, N + 8, generator=g).to(DT[out][1])
+        self.block_m = block_m
+        for k in ("x", "a", "b", "ranks", "scales", "add"):
+            v = getattr(self, k)
+            setattr(self, k, None if v is None else v.to(DEV))
+        self.ad = runner.LoraAdapters(T, K, R, L, dtype, block_m)
+        self.ad.plan(self.ids.to(DEV))
+
+    def reference(self, addend):
+        xn, an, bn = _np(self.x)[:, :self.K], _np(self.a), _np(self.b)
+        ids = self.ids.numpy()
+        ranks = None if self.ranks is None else self.ranks.cpu().numpy()
+        sc = None if self.scales is None else _np(self.scales)
+        add = _np(self.add)[:, :self.N] if addend else None
+        ref = B.lora(xn, an, bn, ids, ranks, sc, add)
+        err = np.zeros_like(ref) if add is None else U * np.abs(add)
+        for t, i in enumerate(ids):
+            if 0 <= i < self.L:
+                r = self.R if ranks is None else ranks[i]
+                s = 1.0 if sc is None else sc[i]
+                v = np.abs(an[i, :r] @ xn[t]) * s
+                ev = self.K * U * (np.abs(an[i, :r]) @ np.abs(xn[t])) * s + 2.0 ** -16 * v
+                ev += 2.0 ** -24 * (v.max() if r else 0.0)
+                bm = np.abs(bn[i, :, :r])
+                err[t] += bm @ ev + 2 * (self.R + 2) * U * (bm @ (v + ev))
+        return ref, err
+
+    def run(self, addend=True, inplace=False, stream=None):
+        T, K, N, ad = self.T, self.K, self.N, self.ad
+        out = self.add.clone() if inplace else torch.full((T, N + 8), 7.0, dtype=DT[self.out][1],
+                                                          device=DEV)
+        add = out if inplace else self.add if addend else None
+        ws = torch.full((qm.moe_lora_workspace_bytes(T, K, self.R, self.L, self.block_m),), 0xFF,
+                        dtype=torch.uint8, device=DEV)
+        before = out.clone()
+        qm.moe_lora_add(self.x, K + 8, self.a, self.b, self.ranks, self.scales, DT[self.dtype][0],
+                        None if inplace else ad.adapter_ids, ad.sorted_token_ids, ad.expert_ids,
+                        ad.num_tokens_post_padded, T, K, N, self.R, self.L, self.block_m, add,
+                        DT[self.out][0], out, N + 8, ws, stream=stream)
+        assert torch.equal(out[:, N:], before[:, N:])
+        return out[:, :N]
+
+    def check(self, addend=True, inplace=False):
+        ref, err = self.reference(addend or inplace)
+        got = _np(self.run(addend, inplace))
+        assert np.isfinite(got).all()
+        tol = err + HALF[self.out] * (np.abs(ref) + err) + TINY[self.out]
+        worst = np.max(np.abs(got - ref) / tol)
+        assert worst <= 1.0, worst
+
+
+CASES = [
+    (1, 8, 8, 8, 1, 16, 0), (1, 4096, 264, 16, 8, 16, 5), (1, 72, 72, 128, 3, 16, -1),
+    (7, 264, 136, 24, 5, 16, "random"), (64, 1032, 520, 64, 100, 16, "random"),
+    (64, 1032, 520, 64, 100, 16, 3), (100, 4104, 72, 8, 2, 32, "random"),
+    (333, 200, 776, 40, 128, 64, "random"), (1000, 520, 264, 128, 3, 128, "runs"),
+    (517, 64, 64, 16, 4, 256, "random"), (16, 128, 8, 8, 1, 16, 0), (17, 136, 16, 16, 1, 16, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"),
+                                       ("f16", "f32"), ("bf16", "f16")])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_lora(case, dtype, out):
+    T, K, N, R, L, block_m, ids = case
+    print(f"\n[lora] {case} {dtype} {out}", flush=True)
+    c = Case(T, K, N, R, L, dtype, out, block_m, ids)
+    c.check()
+    c.check(inplace=True)
+    c.check(addend=False)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_lora_without_ranks_and_scales(T):
+    Case(T, 520, 200, 32, 6, "bf16", "f32", 16, "random", False, False).check()
+
+
+@pytest.mark.parametrize("std", [2.0 ** -18, 500.0])
+def test_lora_of_small_and_large_inputs_in_fp16(std):
+    """The inner vector leaves fp16's range or its normal numbers; the result does not."""
+    Case(40, 520, 200, 32, 6, "f16", "f32", 16, "random", std=std).check()
+
+
+def test_lora_infinite_input_stays_in_its_token():
+    c = Case(20, 64, 72, 16, 2, "bf16", "f32", 16, "runs", False, False)
+    good = c.run().clone()
+    c.x[3, 5] = float("inf")
+    c.x[11, 0] = float("nan")
+    bad = c.run()
+    rest = [t for t in range(20) if t not in (3, 11)]
+    assert torch.equal(bad[rest], good[rest])
+    assert not bool(torch.isfinite(bad[3]).any()) and bool(torch.isnan(bad[11]).all())
+
+
+def test_labels_and_tokens_out_of_range_are_left_out():
+    c = Case(20, 64, 72, 16, 2, "bf16", "bf16", 16, 1, False, False)
+    c.ad.sorted_token_ids[0] = 1 << 30
+    c.ad.sorted_token_ids[1] = -4
+    c.ad.expert_ids[1] = 77
+    out = c.run(inplace=True)
+    first = c.ids.numel()
+    keep = [0, 1] + list(range(16, first))            # named twice wrongly, in the block labelled 77
+    assert torch.equal(out[keep], c.add[keep, :72])
+    assert not torch.equal(out[2:16], c.add[2:16, :72])
+
+
+def test_int8_linear_with_adapters():
+    T, K, N, R, L = 33, 128, 200, 16, 3
+    g = _rng("int8")
+    lin = runner.Int8Linear(T, K, N)
+    x = torch.randn(T, K, generator=g).to(torch.bfloat16).to(DEV)
+    w_q, w_s = runner.quantize_weights((torch.randn(1, N, K, generator=g) * K ** -0.5).to(DEV), "int8")
+    base = lin.forward(x, w_q[0], w_s[0]).clone()
+    c = Case(T, K, N, R, L, "bf16", "bf16", 16, "random")
+    got = lin.forward(x, w_q[0], w_s[0], lora=(c.ad, c.a, c.b, c.scales, c.ranks))
+    c.x[:, :K] = x
+    c.add[:, :N] = base
+    assert torch.equal(got, c.run())
+    with pytest.raises(AssertionError):
+        lin.forward(x, w_q[0], w_s[0], lora=(c.ad, c.a, c.b[:, :64], c.scales, c.ranks))
+
+
+def test_a_plan_for_more_features_serves_fewer():
+    big = runner.LoraAdapters(9, 4096, 16, 4)
+    ids = torch.arange(9, dtype=torch.int32, device=DEV) % 4
+    big.plan(ids)
+    c = Case(9, 264, 72, 16, 4, "bf16", "f32", 16, "random", False, False)
+    small = runner.LoraAdapters(9, 264, 16, 4)
+    small.plan(ids)
+    x = c.x[:, :264]
+    a = big.add(x, c.a, c.b, torch.empty(9, 72, device=DEV))
+    b = small.add(x, c.a, c.b, torch.empty(9, 72, device=DEV))
+    assert torch.equal(a, b)
+    with pytest.raises(AssertionError):
+        small.add(torch.zeros(9, 512, dtype=torch.bfloat16, device=DEV),
+                  torch.zeros(4, 16, 512, dtype=torch.bfloat16, device=DEV), c.b, a)
