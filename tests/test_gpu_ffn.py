@@ -94,6 +94,12 @@ SHAPES = [
     ([1] * 60 + [0] * 4, 0, 0, 96, 64),
     ([600, 300], 0, 0, 512, 776),
     ([1030, 0, 513, 255], 3, 2, 264, 1032),
+    # 128 x 128 and 256 x 256 tiles in the one direction or the other, ends everywhere
+    ([150, 0, 131, 257], 2, 1, 264, 2056),
+    ([150, 131, 0, 257], 0, 3, 4104, 136),
+    ([300, 0, 513, 259], 1, 0, 712, 8200),
+    ([129, 385, 0, 558], 0, 2, 8200, 712),
+    ([40, 0, 700, 1, 300], 0, 0, 2312, 2056),
 ]
 
 
@@ -165,7 +171,9 @@ def _act_error(gv, kind):
     z = gv if kind == 0 else 2 * c * (gv + 0.044715 * gv ** 3)
     dz = 1.0 if kind == 0 else 2 * c * (1 + 3 * 0.044715 * gv * gv)
     s = 1.0 / (1.0 + np.exp(-np.clip(z, -700, 700)))
-    es = s * ((1 - s) * (np.abs(z) + 4) + 1) * 2.0 ** -22     # of the sigmoid
+    # of the sigmoid; below 2^-126 it may be 0 (the exponential's argument passes 87.3, its
+    # value float32's range from 88.7 on), which is off by 2^-126 at most
+    es = s * ((1 - s) * (np.abs(z) + 4) + 1) * 2.0 ** -22 + 2.0 ** -126
     a = np.abs(gv) * s
     ea = np.abs(gv) * es + a * 2.0 ** -23
     eda = es + np.abs(dz) * (ea * (1 - s) + a * (es + (1 - s) * 2.0 ** -21))
