@@ -172,11 +172,18 @@ __device__ __forceinline__ void store_tile(const GroupedArgs &p, int e, int lo, 
       }
     } else if constexpr (kEpi == kStore) {
       uint16_t *out = (uint16_t *)p.out + e * p.out_expert + row * p.ldo;
+      if constexpr (FJ == 1) {
+        const int n0 = col0 + 4 * g;
+        const f32x4 &v = acc[i][0];
+        if (ok && n0 < p.ncol)
+          *reinterpret_cast<i32x2 *>(out + n0) = i32x2{Ty::pack(v[0], v[1]), Ty::pack(v[2], v[3])};
+      } else {
 #pragma unroll
-      for (int j = 0; j < FJ; j += 2) {
-        const int n0 = col0 + 16 * j + pair;
-        const i32x4 v = join8<Ty>(acc[i][j], acc[i][j + 1]);
-        if (ok && n0 < p.ncol) *reinterpret_cast<i32x4 *>(out + n0) = v;
+        for (int j = 0; j < FJ; j += 2) {
+          const int n0 = col0 + 16 * j + pair;
+          const i32x4 v = join8<Ty>(acc[i][j], acc[i][j + 1]);
+          if (ok && n0 < p.ncol) *reinterpret_cast<i32x4 *>(out + n0) = v;
+        }
       }
     } else if constexpr (kEpi == kGatedUp && FJ % 4 == 0) {
 #pragma unroll
@@ -741,14 +748,141 @@ __global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
   wait_dma_all();                                     // no copy into LDS outlives the workgroup
 }
 
+// ---- a few rows an expert: weights through each wavefront's own LDS -----------------
+// One workgroup of four wavefronts per expert and 16 columns (of both projections, or 16 C
+// of a linear); it takes 16 MB of the expert's rows at a time.  The wavefronts share out
+// the contraction, 64 of it each in turn, and add their sums through LDS at the end;
+// until then each waits for nothing but its own copies, D steps ahead, so that those are
+// always under way: what a product bound by its weights needs.  A step's rows come as
+// whole 128-byte lines.
+constexpr int kStreamWaves = 4;
+
+template <typename Ty, int kEpi, int MB, int C, int D>
+__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(const GroupedArgs p, int col_tiles) {
+  constexpr int kSlot = 16 * (MB + C) * 128, kRingB = kStreamWaves * D * kSlot;
+  constexpr int kPieces = 2 * (MB + C);
+  constexpr int kPartB = kStreamWaves * MB * C * 1024;
+  static_assert((D - 1) * kPieces < 64, "the copies in flight are counted in 6 bits");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kRingB > kPartB ? kRingB : kPartB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, r16 = lane & 15;
+  const int e = blockIdx.x / col_tiles;
+  constexpr int kTN = kEpi == kGatedUp ? 16 : 16 * C;
+  const int n0 = (blockIdx.x - e * col_tiles) * kTN;
+  const int lo = p.off ? min(max(p.off[e], 0), p.rows) : 0;
+  const int hi = p.off ? min(max(p.off[e + 1], lo), p.rows) : p.rows;
+
+  // chunk c of LDS row r lies at c ^ ((r >> 1) & 7)
+  const uint16_t *w0 = p.c + e * p.c_expert + n0 * p.ldc;
+  const int ch = (lane & 7) ^ (lane >> 4);            // of the even copies; the odd ones': ^ 4
+  uint32_t w_off[2 * C];
+#pragma unroll
+  for (int u = 0; u < 2 * C; ++u) {
+    const int col = kEpi == kGatedUp ? 8 * (u & 1) + (lane >> 3) : 8 * u + (lane >> 3);
+    w_off[u] = n0 + col < p.ncol ? 2u * ((uint32_t)col * (uint32_t)p.ldc + 8u * (uint32_t)(ch ^ (4 * (u & 1)))) : kOut;
+  }
+  const uint32_t mine = lds_addr(s_ring) + (uint32_t)(wave * D * kSlot);
+  const int steps = (p.depth + 63) >> 6;
+  const int n = (steps - wave + kStreamWaves - 1) / kStreamWaves;    // this wavefront's
+  const int turn = n > 0 ? (int)(blockIdx.x / kXcds) % n : 0;        // .. from another on in each workgroup
+  typedef __attribute__((address_space(3))) i32x4 *LdsV;
+
+  for (int m0 = lo; m0 < hi; m0 += 16 * MB) {
+    const uint16_t *a0 = p.r + m0 * p.ldr;
+    uint32_t a_off[2 * MB];
+#pragma unroll
+    for (int u = 0; u < 2 * MB; ++u) {
+      const int r = 8 * u + (lane >> 3);
+      a_off[u] = m0 + r < hi ? 2u * ((uint32_t)r * (uint32_t)p.ldr + 8u * (uint32_t)(ch ^ (4 * (u & 1)))) : kOut;
+    }
+    auto copy = [&](int slot, int i) QMOE_INLINE {
+      int at = turn + i;
+      at = at < n ? at : at - n;
+      const int k0 = 64 * (at * kStreamWaves + wave), left = p.depth - k0;
+      const uint32_t to = mine + (uint32_t)(slot * kSlot);
+#pragma unroll
+      for (int u = 0; u < 2 * C; ++u)
+        dma16z(w0 + k0 + (kEpi == kGatedUp && u >= 2 ? (long long)p.H * p.ldc : 0),
+               8 * (ch ^ (4 * (u & 1))) < left ? w_off[u] : kOut, to + 16 * MB * 128 + u * 1024);
+#pragma unroll
+      for (int u = 0; u < 2 * MB; ++u)
+        dma16z(a0 + k0, 8 * (ch ^ (4 * (u & 1))) < left ? a_off[u] : kOut, to + u * 1024);
+    };
+    f32x4 acc[MB][C];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < C; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < n) copy(d, d);
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+      if (i + D <= n) wait_dma<(D - 1) * kPieces>();
+      else wait_dma_all();
+      const uint32_t from = mine + (uint32_t)(slot * kSlot + r16 * 128);
+      i32x4 fa[MB][2], fw[C][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = from + (uint32_t)(((4 * h + g) ^ ((r16 >> 1) & 7)) << 4);
+#pragma unroll
+        for (int j = 0; j < C; ++j) fw[j][h] = *(LdsV)(uintptr_t)(at + (MB + j) * 2048);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) fa[b][h] = *(LdsV)(uintptr_t)(at + b * 2048);
+      }
+      wait_lds();                                     // the slot has been read
+      if (i + D < n) copy(slot, i + D);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int b = 0; b < MB; ++b) acc[b][j] = mfma16<Ty>(fw[j][h], fa[b][h], acc[b][j]);
+      slot = slot + 1 < D ? slot + 1 : 0;
+    }
+    __syncthreads();                                  // every wavefront is done with its ring
+    f32x4 *part = reinterpret_cast<f32x4 *>(s_ring);
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int j = 0; j < C; ++j) part[(wave * MB * C + b * C + j) * 64 + lane] = acc[b][j];
+    __syncthreads();
+    for (int b = wave; b < MB; b += kStreamWaves) {
+      f32x4 sum[1][C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        sum[0][j] = part[(b * C + j) * 64 + lane];
+#pragma unroll
+        for (int v = 1; v < kStreamWaves; ++v) sum[0][j] += part[(v * MB * C + b * C + j) * 64 + lane];
+      }
+      store_tile<Ty, kLinear, kEpi, 1, C>(p, e, lo, m0 - lo + 16 * b, hi - lo, n0, sum);
+    }
+    __syncthreads();                                  // the sums are read: the ring is free
+  }
+}
+
 constexpr int kCus = 256;
 
-// Which kernel: by the tiles that the experts' average rows give.  256 x 256 tiles where
-// half of the CUs have one (E = 8, rows of 2048 x 4096 x 14336: 128 tiles of the linear
-// back down 366 us, with 128 x 128 499; 777 x 1024 x 3584, 70 tiles, 28 us, with 128 x 128
-// 16); else 128 x 128 where these are 192 at least, else 64 x 64 (777 x 1792 x 1024 in 5
-// experts, 80 tiles of 128: 22 us, with 64 x 64 14; 2048 x 4096 x 2048 in 4, 256 tiles: 72,
-// with 64 x 64 112).
+template <typename Ty, int kEpi, int MB, int C, int D>
+hipError_t launch_stream(const GroupedArgs &a, hipStream_t s) {
+  const int tn = kEpi == kGatedUp ? 16 : 16 * C, cols = (a.ncol + tn - 1) / tn;
+  hipLaunchKernelGGL((stream_kernel<Ty, kEpi, MB, C, D>), dim3((unsigned)cols * a.E), dim3(64 * kStreamWaves), 0, s,
+                     a, cols);
+  return hipGetLastError();
+}
+
+// Which kernel, by the experts' average rows (of one expert: its rows; of several the
+// fullest is taken to have twice the average).
+//   A linear of up to 64 rows: weights streamed past 16, 32 or 64 of them (up and down of
+//   one token, 4096 x 14336: 37.7 + 18.8 us, in tiles 43.3 + 57.1; 128 rows in 8 experts of
+//   4096 x 7168: 156 + 95 us with 32 rows, 192 + 107 with 16, 186 + 92 with 64, 206 + 156 in
+//   tiles; 320 rows: 205 + 103 with 64, 218 + 159 in tiles).
+//   Else 256 x 256 tiles where half of the CUs have one (E = 8, rows of 2048 x 4096 x 14336:
+//   128 tiles of the linear back down 366 us, with 128 x 128 499; 777 x 1024 x 3584, 70 tiles,
+//   28 us, with 128 x 128 16), 128 x 128 where these are 192 at least, 64 x 64 below (777 x
+//   1792 x 1024 in 5 experts, 80 tiles of 128: 22 us, with 64 x 64 14; 2048 x 4096 x 2048 in 4,
+//   256 tiles: 72, with 64 x 64 112).
 template <typename Ty, int kLayout, int kEpi>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   auto tiles = [&](int T) {
@@ -757,6 +891,13 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
     return m * ((a.ncol + tn - 1) / tn);
   };
   const dim3 block(256);
+  if constexpr (kLayout == kLinear) {
+    constexpr int C = kEpi == kGatedUp ? 2 : 1;
+    const int most = a.E == 1 ? a.rows : 2 * ((a.rows + a.E - 1) / a.E);
+    if (most <= 16) return launch_stream<Ty, kEpi, 1, C, 5 - C>(a, s);
+    if (most <= 32) return launch_stream<Ty, kEpi, 2, C, 4 - C>(a, s);
+    if (most <= (a.E == 1 ? 64 : 96)) return launch_stream<Ty, kEpi, 4, 2, 3>(a, s);
+  }
   if (tiles(256) >= kCus / 2) {
     hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi>), dim3(kCus), block, 0, s, a);
   } else if (tiles(128) >= 192) {
