@@ -3,7 +3,9 @@
 //
 // Memory streams: a workgroup holds a whole row in registers (eight columns a
 // thread and chunk, 16-byte loads and stores), so every byte is read and written
-// once; the two sums of a row go through one wavefront reduction and LDS.
+// once; the two sums of a row go through one wavefront reduction and LDS.  4096 rows of
+// 4096 with two slots, norms before and after (168 MB): 29.5 us, 5.7 TB/s; the gradients
+// of 8192 rows of 6144 (604 MB): 154 us and 5 for the weights' sums.
 #include "qmoe_block.h"
 #include "qmoe_device.h"
 
@@ -121,11 +123,45 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs p) {
   }
 }
 
+// Eight neighbouring values as they lie in memory.
+template <typename Ty>
+struct Packed {
+  i32x4 q[sizeof(typename Ty::T) == 4 ? 2 : 1];
+};
+template <typename Ty>
+__device__ __forceinline__ Packed<Ty> load_packed(const void *base, long long at) {
+  Packed<Ty> v;
+  if constexpr (sizeof(typename Ty::T) == 4) {
+    const i32x4 *p = reinterpret_cast<const i32x4 *>((const float *)base + at);
+    v.q[0] = p[0];
+    v.q[1] = p[1];
+  } else {
+    v.q[0] = *reinterpret_cast<const i32x4 *>((const uint16_t *)base + at);
+  }
+  return v;
+}
+template <typename Ty>
+__device__ __forceinline__ f32x8 unpack(const Packed<Ty> &v) {
+  if constexpr (sizeof(typename Ty::T) == 4) {
+    f32x8 f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __int_as_float(v.q[i >> 2][i & 3]);
+    return f;
+  } else {
+    return unpack8<Ty>(v.q[0]);
+  }
+}
+
 // Workgroup b takes tokens b, b + grid, ..; the weights' gradients are added up
 // column by column in registers and left, one row of each workgroup, in the
-// workspace: [3][grid][N] (w_pre, w_post, channel gate).
+// workspace: [3][grid][N] (w_pre, w_post, channel gate).  A row's two sums wait for
+// its loads and for each other, so the next row's loads go out before them.
+// (8192 rows of 6144: 259 us without, 165 with two chunks a thread, of whose workgroups a CU
+// holds one of six wavefronts.  Rows of more than 8192 need two chunks of 1024 threads, whose
+// registers do not hold the next row.)
 template <typename Ty, typename Res, int V>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBwdArgs p) {
+  constexpr bool kAhead = V == 1;
   __shared__ float s_part[4][16];
   const int N = p.N, chunks = N / 8;
   const float inv = 1.0f / (float)N;
@@ -133,31 +169,64 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBwdArgs p
   f32x8 g_pre[V], g_post[V], g_gate[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) g_pre[i] = g_post[i] = g_gate[i] = zero8();
-  int turn = 0;
-  for (long long t = blockIdx.x; t < p.M; t += gridDim.x, turn ^= 2) {
-    f32x8 dr[V], s[V];
-    const float f = p.w_pre ? p.rstd_pre[t] : 0.0f;
+  struct Row {
+    Packed<Res> dr[V], r[V];
+    Packed<Ty> dh[V], y[V];                           // y: the first slot
+    float f_pre, f_post, gate;
+  } next;
+  auto fetch = [&](long long t) __attribute__((always_inline)) {
+    if (p.w_pre) next.f_pre = p.rstd_pre[t];
+    if (p.w_post) next.f_post = p.rstd_post[t];
+    if (p.gate_kind == MOE_GATE_TOKEN) next.gate = p.gate[t];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      dr[i] = p.d_r && c < chunks ? load8<Res>(p.d_r, t * N + 8 * c) : zero8();
-      s[i] = p.y && c < chunks ? slots8<Ty>(p.y, p.top_k, t, N, c) : zero8();
+      if (c < chunks) {
+        const long long at = t * N + 8 * c;
+        if (p.w_pre) {
+          next.r[i] = load_packed<Res>(p.r, at);
+          next.dh[i] = load_packed<Ty>(p.d_h, at);
+        }
+        if (p.d_r) next.dr[i] = load_packed<Res>(p.d_r, at);
+        if (p.y) next.y[i] = load_packed<Ty>(p.y, t * p.top_k * N + 8 * c);
+      }
     }
-    if (p.w_pre) {
-      f32x8 n[V], d[V];
-      float q = 0.0f;
+  };
+  int turn = 0;
+  long long t = blockIdx.x;
+  if (kAhead) fetch(t);
+  for (; t < p.M; t += gridDim.x, turn ^= 2) {
+    if (!kAhead) fetch(t);
+    const float f = next.f_pre, fp = p.w_post ? next.f_post : 1.0f;
+    const float gate_t = p.gate_kind == MOE_GATE_TOKEN ? next.gate : 1.0f;
+    f32x8 dr[V], s[V], n[V], d[V];
+    float q = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        n[i] = d[i] = zero8();
-        if (c < chunks) {
-          n[i] = load8<Res>(p.r, t * N + 8 * c) * f;
-          const f32x8 dh = load8<Ty>(p.d_h, t * N + 8 * c);
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      dr[i] = s[i] = n[i] = d[i] = zero8();
+      if (c < chunks) {
+        if (p.d_r) dr[i] = unpack<Res>(next.dr[i]);
+        if (p.y) s[i] = unpack<Ty>(next.y[i]);
+        if (p.w_pre) {
+          n[i] = unpack<Res>(next.r[i]) * f;
+          const f32x8 dh = unpack<Ty>(next.dh[i]);
           g_pre[i] += dh * n[i];
           d[i] = dh * load8<TypeF32>(p.w_pre, 8 * c);
           q += sum8(d[i] * n[i]);
         }
       }
+    }
+    if (kAhead && t + gridDim.x < p.M) fetch(t + gridDim.x);
+    if (p.y && p.top_k > 1) {                         // the slots added in their order
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < chunks)
+          for (int j = 1; j < p.top_k; ++j) s[i] += load8<Ty>(p.y, (t * p.top_k + j) * N + 8 * c);
+      }
+    }
+    if (p.w_pre) {
       const float mean = row_sum(q, s_part[turn]) * inv;
 #pragma unroll
       for (int i = 0; i < V; ++i) dr[i] += f * (d[i] - n[i] * mean);
@@ -170,9 +239,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBwdArgs p
       }
     }
     if (!p.y) continue;
-    // u = gate * sum dr p / .. is both the token gate's gradient and the norm's mean
-    const float fp = p.w_post ? p.rstd_post[t] : 1.0f;
-    const float gate_t = p.gate_kind == MOE_GATE_TOKEN ? p.gate[t] : 1.0f;
+    // the sum of dr p (by the channel gate) is both the token gate's gradient and, times it,
+    // the norm's mean
     float u = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -217,25 +285,34 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBwdArgs p
   }
 }
 
-// The workgroups' rows added up, in their order: 64 columns a workgroup, four
-// quarters of the rows.
-__global__ __launch_bounds__(256) void norm_join_kernel(const NormBwdArgs p, int rows) {
-  __shared__ float s_part[4][64];
+// The workgroups' rows added up in a fixed order: 64 columns a workgroup, its 16
+// wavefronts a sixteenth of the rows each (four of them with a quarter: 33 us for 512
+// rows of 6144 where this takes 9).
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves) void norm_join_kernel(const NormBwdArgs p, int rows) {
+  __shared__ float s_part[kJoinWaves][64];
   float *const outs[3] = {p.d_w_pre, p.d_w_post, p.gate_kind == MOE_GATE_CHANNEL ? p.d_gate : nullptr};
   float *out = outs[blockIdx.y];
   if (!out) return;
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
-  float v = 0.0f;
+  const int lane = threadIdx.x & 63, col = blockIdx.x * 64 + lane, part = threadIdx.x >> 6;
+  float v[4] = {};
   if (col < p.N) {
     const float *ws = p.ws + (long long)blockIdx.y * rows * p.N + col;
-    const int from = rows * part / 4, to = rows * (part + 1) / 4;
-    for (int r = from; r < to; ++r) v += ws[(long long)r * p.N];
+    const int to = rows * (part + 1) / kJoinWaves;
+    int r = rows * part / kJoinWaves;
+    for (; r + 4 <= to; r += 4)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += ws[(long long)(r + i) * p.N];
+    for (; r < to; ++r) v[0] += ws[(long long)r * p.N];
   }
-  s_part[part][threadIdx.x & 63] = v;
+  s_part[part][lane] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
-  if (part == 0 && col < p.N)
-    out[col] = (s_part[0][threadIdx.x] + s_part[1][threadIdx.x]) +
-               (s_part[2][threadIdx.x] + s_part[3][threadIdx.x]);
+  if (part == 0 && col < p.N) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) sum += s_part[w][lane];
+    out[col] = sum;
+  }
 }
 
 // threads for rows of N columns with at most `most` chunks a thread
@@ -246,7 +323,12 @@ int threads_for(int N, int most) {
   return t;
 }
 
-int backward_grid(int M) { return M < 512 ? M : 512; }
+// As many workgroups as the card holds at once (a CU one where rows of more than 4096 take
+// nine wavefronts or more), fewer where that gives each the same number of tokens.
+int backward_grid(int M, int N) {
+  const int most = N > 4096 ? 256 : 512, each = (M + most - 1) / most;
+  return each ? (M + each - 1) / each : 0;
+}
 
 template <typename Ty, typename Res>
 hipError_t run(const NormArgs &a, hipStream_t s) {
@@ -258,9 +340,9 @@ hipError_t run(const NormArgs &a, hipStream_t s) {
 }
 template <typename Ty, typename Res>
 hipError_t run_backward(const NormBwdArgs &a, hipStream_t s) {
-  const int rows = backward_grid(a.M);
+  const int rows = backward_grid(a.M, a.N);
   if (a.M > 0) {
-    const int t = threads_for(a.N, 2);
+    const int t = threads_for(a.N, 1);
     const dim3 grid(rows), block(t);
     if (a.N / 8 <= t) hipLaunchKernelGGL((norm_backward_kernel<Ty, Res, 1>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((norm_backward_kernel<Ty, Res, 2>), grid, block, 0, s, a);
@@ -269,14 +351,14 @@ hipError_t run_backward(const NormBwdArgs &a, hipStream_t s) {
   }
   const bool sums = a.d_w_pre || a.d_w_post || (a.d_gate && a.gate_kind == MOE_GATE_CHANNEL);
   if (!sums) return hipSuccess;
-  hipLaunchKernelGGL(norm_join_kernel, dim3((a.N + 63) / 64, 3), dim3(256), 0, s, a, rows);
+  hipLaunchKernelGGL(norm_join_kernel, dim3((a.N + 63) / 64, 3), dim3(64 * kJoinWaves), 0, s, a, rows);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int M, int N) {
-  return (size_t)3 * backward_grid(M) * N * sizeof(float);
+  return (size_t)3 * backward_grid(M, N) * N * sizeof(float);
 }
 
 hipError_t launch_norm(const NormArgs &a, int dtype, int r_dtype, hipStream_t s) {
