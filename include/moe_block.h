@@ -106,7 +106,8 @@ size_t moe_lora_workspace_bytes(int T, int K, int R, int L, int block_m);
  * 1, block_m, 0, ...), once for all the projections of a step.  Rows of a and
  * columns of b from r on are not used, whatever they hold.  The inner vector
  * a x_t is float32 and enters the second product in two 16-bit parts (2^-16 of
- * its value is left out at most); the result is rounded once.
+ * its value is left out at most; three parts where out is float32, 2^-23); the
+ * result is rounded once.
  *
  *   x       [T, K] of type dtype (MOE_BF16, MOE_F16), rows ldx elements apart
  *   a       [L, R, K], b [L, N, R] of type dtype

@@ -197,7 +197,9 @@ template <typename Ty, typename Out, int S>
 __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kernel(const LoraArgs p, int splits, int blocks) {
   typedef typename Out::T T;
   constexpr int kRow = 32 * S + 8;                    // 16-bit values of an LDS row: off the banks
-  __shared__ __attribute__((aligned(16))) uint16_t s_hi[kTokens][kRow], s_lo[kTokens][kRow];
+  // two parts leave out 2^-16 of v, or for float32 results three less than its own rounding
+  constexpr int kParts = sizeof(T) == 4 ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) uint16_t s_v[kParts][kTokens][kRow];
   __shared__ float s_up[kTokens];
   __shared__ int s_tok[kTokens];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r16 = lane & 15;
@@ -280,8 +282,8 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
       }
   }
   for (int m0 = 0; m0 < p.block_m; m0 += tokens) {
-    // v in two 16-bit parts; for fp16 through a power of two that brings a token's largest
-    // value near 1, so that both parts of every value lie in its range
+    // v in 16-bit parts; for fp16 through a power of two that brings a token's largest
+    // value near 1, so that the parts of every value lie in its range
     float top = 0.0f, down = scale, up = 1.0f;
 #pragma unroll
     for (int i = 0; i < kQuads; ++i)
@@ -304,17 +306,19 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
     for (int i = 0; i < kQuads; ++i) {
       const int r = 4 * (part + i * each);
       if (r < 32 * S) {
-        i32x2 hi, lo;
+        float rest[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float a0 = v[i][2 * q] * down, a1 = v[i][2 * q + 1] * down;
-          hi[q] = Ty::pack(a0, a1);
-          const float h0 = Ty::load((uint16_t)hi[q]), h1 = Ty::load((uint16_t)((uint32_t)hi[q] >> 16));
-          // nothing is left of an infinity
-          lo[q] = Ty::pack(__builtin_isfinite(h0) ? a0 - h0 : 0.0f, __builtin_isfinite(h1) ? a1 - h1 : 0.0f);
+        for (int q = 0; q < 4; ++q) rest[q] = v[i][q] * down;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const i32x2 w = {Ty::pack(rest[0], rest[1]), Ty::pack(rest[2], rest[3])};
+          *reinterpret_cast<i32x2 *>(&s_v[k][mine][r]) = w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float h = Ty::load((uint16_t)((uint32_t)w[q >> 1] >> (16 * (q & 1))));
+            rest[q] = __builtin_isfinite(h) ? rest[q] - h : 0.0f;    // nothing is left of an infinity
+          }
         }
-        *reinterpret_cast<i32x2 *>(&s_hi[mine][r]) = hi;
-        *reinterpret_cast<i32x2 *>(&s_lo[mine][r]) = lo;
       }
     }
     if (part == 0) {
@@ -352,12 +356,12 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         if (32 * s >= rank) break;
-        const i32x4 hi = *reinterpret_cast<const i32x4 *>(&s_hi[m + r16][32 * s + 8 * g]);
-        const i32x4 lo = *reinterpret_cast<const i32x4 *>(&s_lo[m + r16][32 * s + 8 * g]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma16<Ty>(bv[j][s], lo, acc[j]);
+        for (int k = kParts - 1; k >= 0; --k) {       // the smallest first
+          const i32x4 w = *reinterpret_cast<const i32x4 *>(&s_v[k][m + r16][32 * s + 8 * g]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma16<Ty>(bv[j][s], hi, acc[j]);
+          for (int j = 0; j < 4; ++j) acc[j] = mfma16<Ty>(bv[j][s], w, acc[j]);
+        }
       }
       const float by = s_up[m + r16];
 #pragma unroll

@@ -29,7 +29,7 @@ __device__ __forceinline__ f32x8 load8(const void *base, long long at) {
     const f32x4 a = p[0], b = p[1];
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
-    return unpack8<Ty>(*reinterpret_cast<const i32x4 *>((const uint16_t *)base + at));
+    return unpack8<Ty>(__builtin_nontemporal_load(reinterpret_cast<const i32x4 *>((const uint16_t *)base + at)));
   }
 }
 template <typename Ty>
@@ -42,7 +42,7 @@ __device__ __forceinline__ void store8(void *base, long long at, const f32x8 &v)
     i32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = Ty::pack(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<i32x4 *>((uint16_t *)base + at) = o;
+    __builtin_nontemporal_store(o, reinterpret_cast<i32x4 *>((uint16_t *)base + at));
   }
 }
 __device__ __forceinline__ f32x8 zero8() { return f32x8{0, 0, 0, 0, 0, 0, 0, 0}; }
