@@ -329,14 +329,17 @@ __device__ __forceinline__ void dma16s(const i32x4 &src, uint32_t voff, uint32_t
 // Power sets the clock (1.5 to 1.9 GHz); the matrix units are busy about 80% of the time.
 // What is left: the epilogue, during which no products run, tiles that the experts' rows
 // fill in part, and the last round of tiles.
-template <typename Ty, int kLayout, int kEpi>
+template <typename Ty, int kLayout, int kEpi, int TM>
 __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
-  constexpr int T = 256;
+  constexpr int T = 256;                              // columns of a tile
+  constexpr int FI = TM / 32;                         // row fragments of a wavefront
   constexpr bool kRT = kLayout == kWgrad, kCT = kLayout != kLinear;
   constexpr bool kFine = kRT && kCT;                  // stages of 32, four slots
   constexpr int kStage = kFine ? 32 : 64, kSlots = kFine ? 4 : 2;
-  constexpr int kPart = T * 2 * kStage, kSlot = 2 * kPart, kRowB = 2 * T;
-  constexpr int P = kFine ? 4 : 8;                    // copies of a wavefront, stage and operand
+  constexpr int kPart = TM * 2 * kStage, kSlot = kPart + T * 2 * kStage, kRowB = 2 * T;
+  static_assert(TM == T || !kRT, "rows across come in rows of 256");
+  // copies of a wavefront and stage: of the rows, of the columns
+  constexpr int PR = kFine ? 4 : TM / 32, P = kFine ? 4 : 8;
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kSlots * kSlot];
   __shared__ Segments s_seg;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -345,13 +348,13 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   const int g = lane >> 4, r16 = lane & 15;
   constexpr int kTN = kEpi == kGatedUp ? T / 2 : T;
   const int ntn = (p.ncol + kTN - 1) / kTN;
-  const int ntr = (p.nrow + T - 1) / T;               // kWgrad
+  const int ntr = (p.nrow + TM - 1) / TM;             // kWgrad
   // twice 32 of the contraction that a tile takes; without any (an expert without rows)
   // zeros are contracted
   auto pairs = [](int depth) QMOE_INLINE { return max(1, (depth + 63) >> 6); };
   // tiles of an expert with n rows, and what one takes: its pairs, the epilogue as four
   find_segments(s_seg, p.off, p.rows, p.E,
-                [&](int n) { return (kLayout == kWgrad ? ntr : (n + T - 1) / T) * ntn; },
+                [&](int n) { return (kLayout == kWgrad ? ntr : (n + TM - 1) / TM) * ntn; },
                 [&](int n) { return kLayout == kWgrad ? (float)(pairs(n) + 4) : 1.0f; });
 
   // This workgroup's tiles.  The tiles are cut into eight contiguous runs of equal cost, one
@@ -365,7 +368,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
 
   struct Tile {
     int e, lo, nrow, depth, m0, n0;
-    int rows;                                         // of the tile: 256 at most
+    int rows;                                         // of the tile: TM at most
   };
   // tile tt (its expert is e or a later one)
   auto decode = [&](int tt, int e) QMOE_INLINE -> Tile {
@@ -378,13 +381,13 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
     w.depth = kLayout == kWgrad ? n : p.depth;
     const int local = tt - __builtin_amdgcn_readfirstlane(s_seg.first[e]);
     constexpr int kRows = 4;
-    const int ntm = kLayout == kWgrad ? ntr : (n + T - 1) / T;
+    const int ntm = kLayout == kWgrad ? ntr : (n + TM - 1) / TM;
     const int per = kRows * ntn, grp = local / per, rem = local - grp * per;
     const int rows = min(kRows, ntm - grp * kRows);
     const int tn = rem / rows;
-    w.m0 = (grp * kRows + rem - tn * rows) * T;
+    w.m0 = (grp * kRows + rem - tn * rows) * TM;
     w.n0 = tn * kTN;
-    w.rows = min(T, w.nrow - w.m0);
+    w.rows = min(TM, w.nrow - w.m0);
     return w;
   };
 
@@ -395,10 +398,11 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   auto swz = [](int r) QMOE_INLINE { return (r >> 1) & 7; };
   auto swt = [](int k) QMOE_INLINE { return (k & 3) | ((k >> 1) & 4); };
   const uint32_t ring = lds_addr(s_ring);
-  const uint32_t my_ring = __builtin_amdgcn_readfirstlane(ring + (uint32_t)(P * wave * 1024));
+  const uint32_t my_ring = __builtin_amdgcn_readfirstlane(ring + (uint32_t)(PR * wave * 1024));
+  const uint32_t my_cols = kPart + (P - PR) * wave * 1024;            // from there to the columns' part
   // the copies' cursor: stages of tile cur_t that are left, what of its contraction is
   int cur_t = t, cur_left = 0, cur_valid = 0, cur_e = 0;
-  uint32_t cur_slot = my_ring;                        // this wavefront's part of the slot
+  uint32_t cur_slot = my_ring, cur_cols = my_ring + my_cols;          // this wavefront's parts of the slot
   // resources of the cursor's stage: base address (advanced stage by stage), bytes that
   // are memory, format
   i32x4 r_src = {0, 0, (int)kOut, 0x00020000}, c_src = r_src, c_src2 = r_src;
@@ -413,16 +417,16 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
     s[0] = (int)b;
     s[1] = (int)(b >> 32);
   };
-  // Copy u of an operand that runs along the contraction: LDS rows 64 wave + 8 u .. + 7,
-  // of one that runs across it: LDS rows 2 P wave + 2 u, + 1.  A lane's place there:
-  auto row_of = [&](int u) QMOE_INLINE { return 64 * wave + 8 * u + (lane >> 3); };
+  // Copy u of an operand that runs along the contraction: LDS rows 8 (copies wave + u) .. + 7,
+  // of one that runs across it: LDS rows 2 (copies wave + u), + 1.  A lane's place there:
+  auto row_of = [&](int u, int copies) QMOE_INLINE { return 8 * (copies * wave + u) + (lane >> 3); };
   auto along_k = [&](int u) QMOE_INLINE { return 8 * ((lane & 7) ^ swz(8 * u + (lane >> 3))); };
   auto across_k = [&](int u) QMOE_INLINE { return 2 * P * wave + 2 * u + (lane >> 5); };
   auto across_at = [&](int u) QMOE_INLINE {
     const int q = lane & 31;
     return 8 * (((q >> 1 ^ swt(across_k(u))) << 1) | (q & 1));
   };
-  uint32_t r_off[P], c_off[P];                        // bytes from the stage's base, or kOut
+  uint32_t r_off[PR], c_off[P];                       // bytes from the stage's base, or kOut
   auto enter = [&]() QMOE_INLINE {
     const Tile w = decode(cur_t, cur_e);
     cur_e = w.e;
@@ -440,18 +444,22 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
     asm volatile("s_nop 4");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < P; ++u) {
+    for (int u = 0; u < PR; ++u) {
+      const int row = row_of(u, PR);
       if (kRT)
         r_off[u] = across_at(u) < w.rows
                        ? 2u * ((uint32_t)across_k(u) * (uint32_t)p.ldr + (uint32_t)across_at(u)) : kOut;
       else
-        r_off[u] = row_of(u) < w.rows ? 2u * ((uint32_t)row_of(u) * (uint32_t)p.ldr + (uint32_t)along_k(u)) : kOut;
+        r_off[u] = row < w.rows ? 2u * ((uint32_t)row * (uint32_t)p.ldr + (uint32_t)along_k(u)) : kOut;
+    }
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
       if (kCT) {
         c_off[u] = w.n0 + across_at(u) < p.ncol
                        ? 2u * ((uint32_t)across_k(u) * (uint32_t)p.ldc + (uint32_t)across_at(u)) : kOut;
       } else {
         // of both projections: sixteen columns of the gate's, the same of the other's, ..
-        const int at = kEpi == kGatedUp ? (row_of(u) >> 5) * 16 + (row_of(u) & 15) : row_of(u);
+        const int row = row_of(u, P), at = kEpi == kGatedUp ? (row >> 5) * 16 + (row & 15) : row;
         c_off[u] = w.n0 + at < p.ncol ? 2u * ((uint32_t)at * (uint32_t)p.ldc + (uint32_t)along_k(u)) : kOut;
       }
     }
@@ -460,15 +468,15 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   auto cut = [&]() QMOE_INLINE {
     if (cur_valid < kStage) {
 #pragma unroll
-      for (int u = 0; u < P; ++u) {
-        r_off[u] = (kRT ? across_k(u) : along_k(u)) < cur_valid ? r_off[u] : kOut;
-        c_off[u] = (kCT ? across_k(u) : along_k(u)) < cur_valid ? c_off[u] : kOut;
-      }
+      for (int u = 0; u < PR; ++u) r_off[u] = (kRT ? across_k(u) : along_k(u)) < cur_valid ? r_off[u] : kOut;
+#pragma unroll
+      for (int u = 0; u < P; ++u) c_off[u] = (kCT ? across_k(u) : along_k(u)) < cur_valid ? c_off[u] : kOut;
     }
   };
   // The cursor's copies are under way: on to the next stage.  The plain steps first, ..
   auto next_stage = [&]() QMOE_INLINE {
-    cur_slot = my_ring + ((cur_slot - my_ring + kSlot) & (kSlots * kSlot - 1));
+    cur_slot = cur_slot - my_ring == (kSlots - 1) * kSlot ? my_ring : cur_slot + kSlot;
+    cur_cols = cur_slot + my_cols;
     --cur_left;
     cur_valid -= kStage;
     advance(r_src, r_step);
@@ -491,10 +499,11 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   };
   // copy q of the cursor's stage: resource, offset, place in the ring
   auto piece_src = [&](int q) QMOE_INLINE -> const i32x4 & {
-    return q < P ? r_src : kEpi == kGatedUp && (q >> 1 & 1) ? c_src2 : c_src;
+    return q < PR ? r_src : kEpi == kGatedUp && ((q - PR) >> 1 & 1) ? c_src2 : c_src;
   };
-  auto piece_off = [&](int q) QMOE_INLINE { return q < P ? r_off[q] : c_off[q - P]; };
-  auto piece_at = [](int q) QMOE_INLINE { return q < P ? q * 1024 : kPart + (q - P) * 1024; };
+  auto piece_off = [&](int q) QMOE_INLINE { return q < PR ? r_off[q] : c_off[q - PR]; };
+  auto piece_to = [&](int q) QMOE_INLINE { return q < PR ? cur_slot : cur_cols; };
+  auto piece_at = [](int q) QMOE_INLINE { return (q < PR ? q : q - PR) * 1024; };
 
   // ---- fragments.  A stage of 64 is read in halves of 32.
   const uint32_t ch = (uint32_t)((g ^ swz(r16)) << 4);
@@ -502,7 +511,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   const uint32_t tf = (uint32_t)((r16 >> 2) | ((g & 1) << 2));        // swt of the lane's rows
   const uint32_t c_rd = (uint32_t)kPart + (kCT ? tr + (((uint32_t)(wn * 8) ^ tf) << 5)
                                                : (uint32_t)((wn * 128 + r16) * 128) + ch);
-  const uint32_t r_rd = kRT ? tr + (((uint32_t)(wm * 8) ^ tf) << 5) : (uint32_t)((wm * 128 + r16) * 128) + ch;
+  const uint32_t r_rd = kRT ? tr + (((uint32_t)(wm * 8) ^ tf) << 5) : (uint32_t)((wm * (TM / 2) + r16) * 128) + ch;
   typedef __attribute__((address_space(3))) s16x4 *LdsT;
   typedef __attribute__((address_space(3))) i32x4 *LdsV;
   auto read_across = [&](uint32_t at) QMOE_INLINE -> i32x4 {
@@ -512,7 +521,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
     return i32x4{x[0], x[1], y[0], y[1]};
   };
   struct Frags {
-    i32x4 r[8], c[8];
+    i32x4 r[FI], c[8];
   };
   // ra, ca: addresses of the wavefront's first fragments; fragment k: 0 .. 7 of the
   // columns, then of the rows
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   auto half_at = [](uint32_t rd, bool is_across, uint32_t base, bool second) QMOE_INLINE -> uint32_t {
     return is_across ? base + rd + (second ? 32 * kRowB : 0) : (base + rd) ^ (second ? 64u : 0u);
   };
-  f32x4 acc[8][8];
+  f32x4 acc[FI][8];
   // The products of `f`, the first or second half of the stage in hand; the fragments of
   // the half that follows (in slot `base`) come into `nf` on the way, with a second half
   // also the copies of the stage two ahead.  A product takes 16 cycles, another instruction
@@ -531,17 +540,19 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
   auto step = [&](const Frags &f, Frags &nf, uint32_t base, auto second_) QMOE_INLINE {
     constexpr bool second = kFine || decltype(second_)::value;
     if constexpr (second) {
-      wait_dma<kFine ? 2 * 2 * P : 0>();              // the next stage has landed here,
+      wait_dma<kFine ? 2 * (PR + P) : 0>();              // the next stage has landed here,
       wait_lds();                                     // the one in hand is read ...
       phase_end();                                    // ... here and everywhere
     }
+    // between how many products a copy goes out
+    constexpr int kEvery = kFine ? 8 : FI == 8 ? 4 : 3;
     uint32_t ra = 0, ca = 0;
     int read = 0, copy = 0;
 #pragma unroll
-    for (int q = 0; q < 64; ++q) {
-      const int j = q / 8, i = q % 8;
-      if (second && q % (32 / P) == (kFine ? 4 : 1)) {
-        mfma_copy<Ty>(acc[i][j], f.c[j], f.r[i], piece_src(copy), piece_off(copy), cur_slot, piece_at(copy));
+    for (int q = 0; q < 8 * FI; ++q) {
+      const int j = q / FI, i = q % FI;
+      if (second && q % kEvery == kEvery / 2 && copy < PR + P) {
+        mfma_copy<Ty>(acc[i][j], f.c[j], f.r[i], piece_src(copy), piece_off(copy), piece_to(copy), piece_at(copy));
         ++copy;
       } else {
         mfma_into<Ty>(acc[i][j], f.c[j], f.r[i]);
@@ -551,11 +562,11 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
         ca = half_at(c_rd, kCT, base, !second);
         asm volatile("" : "+v"(ra), "+v"(ca));        // 2048 k is added in the instruction
       }
-      if (kFine ? q % 3 == 2 && read < 16 : second ? q % 4 == 3 : q % 2 == 0 && q > 0 && q <= 32) {
+      if (read < FI + 8 && (kFine ? q % 3 == 2 : second ? q % kEvery == kEvery - 1 : q % 2 == 0 && q > 0)) {
         read_frag(nf, ra, ca, read);
         ++read;
       }
-      if (second && q == 62) next_stage();
+      if (second && q == 8 * FI - 1) next_stage();
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (second) next_tile();
@@ -566,22 +577,22 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) {
 #pragma unroll
-    for (int q = 0; q < 2 * P; ++q) dma16s(piece_src(q), piece_off(q), cur_slot, piece_at(q));
+    for (int q = 0; q < PR + P; ++q) dma16s(piece_src(q), piece_off(q), piece_to(q), piece_at(q));
     next_stage();
     next_tile();
   }
-  wait_dma<(kSlots - 1) * 2 * P>();                   // stage 0 has landed here ...
+  wait_dma<(kSlots - 1) * (PR + P)>();                  // stage 0 has landed here ...
   phase_end();                                        // ... and everywhere
   uint32_t base = ring;                               // slot of the stage in hand
-  auto next_base = [&]() QMOE_INLINE { base = ring + ((base - ring + kSlot) & (kSlots * kSlot - 1)); };
+  auto next_base = [&]() QMOE_INLINE { base = base - ring == (kSlots - 1) * kSlot ? ring : base + kSlot; };
   Tile w = decode(t, 0);
   Frags fa, fb;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) read_frag(fa, base + r_rd, base + c_rd, k);
+  for (int k = 0; k < FI + 8; ++k) read_frag(fa, base + r_rd, base + c_rd, k);
   for (;;) {
     const int n = pairs(w.depth);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -596,10 +607,10 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
     // the last products are written before anything else reads their registers
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
-    store_tile<Ty, kLayout, kEpi, 8, 8>(p, w.e, kLayout == kWgrad ? 0 : w.lo, w.m0 + wm * 128, w.nrow,
+    store_tile<Ty, kLayout, kEpi, FI, 8>(p, w.e, kLayout == kWgrad ? 0 : w.lo, w.m0 + wm * (TM / 2), w.m0 + w.rows,
                                         w.n0 + wn * (kTN / 2), acc);
     t += gx;
     if (t >= t_end) break;
@@ -882,13 +893,21 @@ hipError_t launch_stream(const GroupedArgs &a, hipStream_t s) {
 //   128 tiles of the linear back down 366 us, with 128 x 128 499; 777 x 1024 x 3584, 70 tiles,
 //   28 us, with 128 x 128 16), 128 x 128 where these are 192 at least, 64 x 64 below (777 x
 //   1792 x 1024 in 5 experts, 80 tiles of 128: 22 us, with 64 x 64 14; 2048 x 4096 x 2048 in 4,
-//   256 tiles: 72, with 64 x 64 112).
+//   256 tiles: 72, with 64 x 64 112).  Tiles of 192 rows where they need fewer rounds over the
+//   card by more than their products cost (8192 rows in 8 experts, 14336 -> 4096: 3 rounds
+//   either way, 968 us against 1030; 28672 -> 4096 1834 against 1960).
 template <typename Ty, int kLayout, int kEpi>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   auto tiles = [&](int T) {
     const long long each = ((long long)a.rows + a.E - 1) / a.E, tn = kEpi == kGatedUp ? T / 2 : T;
     const long long m = a.E * (((kLayout == kWgrad ? a.nrow : each) + T - 1) / T);
     return m * ((a.ncol + tn - 1) / tn);
+  };
+  // rounds of tiles of TM x 256 over the card; of several experts each leaves a tile half full
+  auto rounds = [&](int TM) {
+    const int tn = kEpi == kGatedUp ? 128 : 256, cols = (a.ncol + tn - 1) / tn;
+    const double m = a.E == 1 ? (double)((a.rows + TM - 1) / TM) : (double)a.rows / TM + 0.5 * a.E;
+    return (double)(long long)((m * cols + kCus - 1) / kCus);
   };
   const dim3 block(256);
   if constexpr (kLayout == kLinear) {
@@ -899,7 +918,13 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
     if (most <= (a.E == 1 ? 64 : 96)) return launch_stream<Ty, kEpi, 4, 2, 3>(a, s);
   }
   if (tiles(256) >= kCus / 2) {
-    hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi>), dim3(kCus), block, 0, s, a);
+    if constexpr (kLayout != kWgrad) {
+      if (rounds(192) * 192 * 1.06 < rounds(256) * 256) {
+        hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi, 192>), dim3(kCus), block, 0, s, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi, 256>), dim3(kCus), block, 0, s, a);
   } else if (tiles(128) >= 192) {
     hipLaunchKernelGGL((square_kernel<Ty, kLayout, kEpi, 128>), dim3(2 * kCus), block, 0, s, a);
   } else {
