@@ -598,6 +598,9 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
         acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         asm volatile("" : "+a"(acc[i][j]));
       }
+    // wait states between a write of a register and the product that adds to it
+    asm volatile("s_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     for (int s = 0; s < n; ++s) {
       if (kFine) next_base();
       step(fa, fb, base, std::false_type{});
@@ -884,7 +887,8 @@ hipError_t launch_stream(const GroupedArgs &a, hipStream_t s) {
 }
 
 // Which kernel, by the experts' average rows (of one expert: its rows; of several the
-// fullest is taken to have twice the average).
+// fullest is taken to have twice the average: how the rows really lie only the device
+// knows, and what they cost, not what comes out, hangs on it).
 //   A linear of up to 64 rows: weights streamed past 16, 32 or 64 of them (up and down of
 //   one token, 4096 x 14336: 37.7 + 18.8 us, in tiles 43.3 + 57.1; 128 rows in 8 experts of
 //   4096 x 7168: 156 + 95 us with 32 rows, 192 + 107 with 16, 186 + 92 with 64, 206 + 156 in

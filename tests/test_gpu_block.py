@@ -160,3 +160,57 @@ def test_named_stream_is_the_one_that_runs():
                          stream=s)
     s.synchronize()
     assert torch.equal(r, ref) and torch.equal(r, (2 * x.float()).to(torch.bfloat16))
+
+
+def test_many_experts_of_which_one_has_all_the_rows():
+    """What is chosen by the average holds for any split."""
+    g = _gen(3)
+    E, Kd, N, rows = 128, 72, 136, 300
+    rnd = lambda *s, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    x, w = rnd(rows, Kd), rnd(E, N, Kd, m=Kd ** -0.5)
+    for e in (0, 63, 127):
+        off = torch.tensor([0] * (e + 1) + [rows] * (E - e), dtype=torch.int32, device=DEV)
+        y, one = (torch.empty(rows, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        qm.moe_grouped_linear(x, Kd, w, 1, off, rows, Kd, N, E, y, N)
+        ref = x.double() @ w[e].double().t()
+        assert float((y.double() - ref).abs().max()) <= 2.0 ** -8 * float(ref.abs().max()) + 1e-4
+        dw = torch.full((E, N, Kd), 7.0, device=DEV)
+        qm.moe_grouped_linear_wgrad(y, N, x, Kd, 1, off, rows, Kd, N, E, 0, dw)
+        ref = y.double().t() @ x.double()
+        assert float((dw[e].double() - ref).abs().max()) <= 1e-3
+        dw[e] = 0
+        assert not bool(dw.any())
+
+
+@pytest.mark.parametrize("rows", [1, 300, 3000])
+def test_grouped_products_of_a_captured_graph_follow_the_offsets(rows):
+    """The experts' rows are read on the device: one graph serves every split."""
+    g = _gen(9)
+    E, Kd, H = 6, 136, 520
+    rnd = lambda *s, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    ffn = runner.GatedFFN(rows, Kd, H, E, train=True)
+    x, dy = rnd(rows, Kd), rnd(rows, Kd)
+    w_up, w_down = rnd(E, 2 * H, Kd, m=Kd ** -0.5), rnd(E, Kd, H, m=H ** -0.5)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+
+    def run():
+        return (ffn.forward(x, w_up, w_down, off),) + ffn.backward(dy, x, w_up, w_down, off)
+
+    run()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            outs = run()
+    for seed in range(4):
+        cuts = torch.randint(0, rows + 1, (E - 1,), generator=torch.Generator().manual_seed(seed))
+        off.copy_(torch.cat([torch.tensor([0]), cuts.sort().values, torch.tensor([rows])]).int())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(bool(torch.isfinite(t.float()).all()) for t in got)

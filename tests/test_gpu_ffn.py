@@ -100,6 +100,8 @@ SHAPES = [
     ([300, 0, 513, 259], 1, 0, 712, 8200),
     ([129, 385, 0, 558], 0, 2, 8200, 712),
     ([40, 0, 700, 1, 300], 0, 0, 2312, 2056),
+    ([990], 7, 3, 136, 12200),
+    ([900], 0, 100, 12200, 72),
 ]
 
 
