@@ -18,7 +18,7 @@ namespace {
 #define QMOE_INLINE __attribute__((always_inline))
 
 constexpr int kWaves = 4;
-constexpr int kMaxShares = 8;
+constexpr int kMaxShares = 4;
 
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
