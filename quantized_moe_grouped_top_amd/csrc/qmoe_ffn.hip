@@ -900,6 +900,11 @@ hipError_t launch_stream(const GroupedArgs &a, hipStream_t s) {
 //   256 tiles: 72, with 64 x 64 112).  Tiles of 192 rows where they need fewer rounds over the
 //   card by more than their products cost (8192 rows in 8 experts, 14336 -> 4096: 3 rounds
 //   either way, 968 us against 1030; 28672 -> 4096 1834 against 1960).
+//   A weight gradient over few rows in few tiles is its prologues and stores, which two
+//   workgroups of 128 x 128 a CU overlap (3584 x 1024 in 5 experts, 280 tiles: 777 rows 17.7
+//   us against 23.8, 12800 rows the same; 2048 x 1408 in 5, 240 tiles, 2048 rows 21.4 against
+//   29.3, but 1792 x 1024, 140 tiles, 3200 rows 25.8 against 24.4; 8192 x 2048 in 4, 1024
+//   tiles, 2048 rows 81.7 against 74.9).
 template <typename Ty, int kLayout, int kEpi>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   auto tiles = [&](int T) {
@@ -921,7 +926,8 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
     if (most <= 32) return launch_stream<Ty, kEpi, 2, C, 4 - C>(a, s);
     if (most <= (a.E == 1 ? 64 : 96)) return launch_stream<Ty, kEpi, 4, 2, 3>(a, s);
   }
-  if (tiles(256) >= kCus / 2) {
+  const bool shallow = kLayout == kWgrad && a.rows <= 512ll * a.E && tiles(256) <= 5 * kCus / 2;
+  if (tiles(256) >= kCus / 2 && !shallow) {
     if constexpr (kLayout != kWgrad) {
       if (rounds(192) * 192 * 1.06 < rounds(256) * 256) {
         hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi, 192>), dim3(kCus), block, 0, s, a);

@@ -263,6 +263,15 @@ def test_gated_down_backward(shape, dtype, act, inplace):
         _untouched(h, (rowmask, H), "h")
 
 
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [([700, 0, 900], 1, 2, 1800, 6152), ([40, 0, 300, 1], 0, 1, 2056, 5000)],
+                         ids=["many rows", "many tiles"])
+def test_weight_gradient_in_the_large_tiles(shape, dtype, out):
+    """256 x 256 tiles: more than 512 rows an expert, and more than 640 tiles."""
+    test_weight_gradient(shape, dtype, out)
+
+
 def test_one_expert_without_offsets_and_no_rows():
     g = _rng("dense")
     K, N, rows = 72, 80, 37
