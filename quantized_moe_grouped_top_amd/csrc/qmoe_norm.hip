@@ -5,7 +5,7 @@
 // thread and chunk, 16-byte loads and stores), so every byte is read and written
 // once; the two sums of a row go through one wavefront reduction and LDS.  4096 rows of
 // 4096 with two slots, norms before and after (168 MB): 29.5 us, 5.7 TB/s; the gradients
-// of 8192 rows of 6144 (604 MB): 154 us and 5 for the weights' sums.
+// of 8192 rows of 6144 (604 MB): 138 us with the weights' sums, 5 of them, 4.4 TB/s.
 #include "qmoe_block.h"
 #include "qmoe_device.h"
 

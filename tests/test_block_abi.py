@@ -42,7 +42,7 @@ def test_block_symbols_and_constants():
 
 @needs_lib
 def test_workspace_sizes():
-    """LoRA: a float32 for every sorted slot, rank and share of K (8 shares of 512 k at
+    """LoRA: a float32 for every sorted slot, rank and share of K (a few shares of 512 k at
     least); norms: three rows of N for each of 512 workgroups at most."""
     for T, K, R, L, b in [(1, 4096, 16, 8, 16), (64, 4096, 64, 32, 16), (4096, 4096, 64, 8, 128),
                           (65536, 64, 128, 128, 256), (1, 8, 8, 1, 16)]:
