@@ -34,6 +34,7 @@ extern "C" {
 #define MOE_MAX_LORA_RANK    128       /* R */
 #define MOE_MAX_NORM_COLUMNS 16384     /* N of the norms */
 #define MOE_MAX_NORM_ROWS    (1 << 24) /* M * top_k of the norms */
+#define MOE_MAX_NORM_VALUES  (1ll << 35) /* M * N of the norms */
 
 /* ======================================================================== *
  * Gated feed-forward of the experts, 16 bits
@@ -156,8 +157,9 @@ int moe_lora_add(const void *x, long long ldx, const void *a, const void *b, con
  *   rstd_post, rstd_pre  [M] float32: 1 / sqrt(mean + eps) of both norms, written
  *            for the backward pass; NULL where not wanted
  * Limits: N a multiple of 8, at most MOE_MAX_NORM_COLUMNS; 0 <= M, 1 <= top_k <=
- * MOE_MAX_TOPK, M * top_k <= MOE_MAX_NORM_ROWS; eps >= 0; all arrays of M x N
- * values, both weights and a channel gate 16-byte aligned. */
+ * MOE_MAX_TOPK, M * top_k <= MOE_MAX_NORM_ROWS, M * N <= MOE_MAX_NORM_VALUES; eps
+ * >= 0; all arrays of M x N values, both weights and a channel gate 16-byte
+ * aligned.  With M = 0 nothing is done, whichever pointers are NULL. */
 int moe_norm_residual(const void *y, int dtype, int top_k, const void *residual, int r_dtype,
                       const float *w_post, const float *gate, int gate_kind, float alpha,
                       float beta, const float *w_pre, float eps, int M, int N, void *r, void *h,
@@ -188,7 +190,8 @@ size_t moe_norm_backward_workspace_bytes(int M, int N);
  *        where not wanted
  *   workspace moe_norm_backward_workspace_bytes(M, N) bytes, 16-byte aligned,
  *        contents on entry ignored, one for each call that may run at the same time
- * Limits as for moe_norm_residual. */
+ * Limits as for moe_norm_residual.  With M = 0 the gradients of the weights and of a
+ * channel gate become 0, whichever other pointers are NULL. */
 int moe_norm_residual_backward(const void *d_r, const void *d_h, const void *y, int dtype,
                                int top_k, const void *r, int r_dtype, const float *w_post,
                                const float *gate, int gate_kind, float alpha, float beta,

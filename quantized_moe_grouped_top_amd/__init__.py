@@ -32,7 +32,7 @@ MOE_MAX_INT8_K, MOE_MAX_INT8_ROWS = 131071, 1 << 27
 MOE_GATED_SILU, MOE_GATED_GELU = 0, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 MOE_MAX_BLOCK_ROWS, MOE_MAX_BLOCK_WIDTH, MOE_MAX_LORA_RANK = 1 << 24, 1 << 20, 128
-MOE_MAX_NORM_COLUMNS, MOE_MAX_NORM_ROWS = 16384, 1 << 24
+MOE_MAX_NORM_COLUMNS, MOE_MAX_NORM_ROWS, MOE_MAX_NORM_VALUES = 16384, 1 << 24, 1 << 35
 
 EXPORTS = [
     "moe_last_error", "moe_last_hip_error", "moe_align_max_padded", "moe_recommended_block_m",

@@ -56,11 +56,14 @@ int check_norm(int dtype, int r_dtype, int top_k, const void *y, int gate_kind, 
   REQUIRE(top_k <= MOE_MAX_TOPK, MOE_EUNSUPPORTED, "%s: top_k=%d above %d", fn, top_k, MOE_MAX_TOPK);
   REQUIRE((long long)M * top_k <= MOE_MAX_NORM_ROWS, MOE_EUNSUPPORTED, "%s: M=%d top_k=%d above %d rows",
           fn, M, top_k, MOE_MAX_NORM_ROWS);
+  REQUIRE((long long)M * N <= MOE_MAX_NORM_VALUES, MOE_EUNSUPPORTED, "%s: M=%d N=%d above %lld values", fn,
+          M, N, MOE_MAX_NORM_VALUES);
   REQUIRE(gate_kind >= MOE_GATE_NONE && gate_kind <= MOE_GATE_TOKEN, MOE_EINVAL,
           "%s: unknown gate %d", fn, gate_kind);
-  REQUIRE((gate_kind == MOE_GATE_NONE) == (gate == nullptr), MOE_EINVAL,
+  // arrays without elements have no address, so that without tokens nothing says which are there
+  REQUIRE((gate_kind == MOE_GATE_NONE) == (gate == nullptr) || M == 0, MOE_EINVAL,
           "%s: gate kind %d and the gate's pointer disagree", fn, gate_kind);
-  REQUIRE(y || gate_kind == MOE_GATE_NONE, MOE_EINVAL, "%s: a gate without a block", fn);
+  REQUIRE(y || gate_kind == MOE_GATE_NONE || M == 0, MOE_EINVAL, "%s: a gate without a block", fn);
   ALIGNED16(y);
   REQUIRE(gate_kind == MOE_GATE_CHANNEL ? aligned16(gate) : aligned4(gate), MOE_EINVAL,
           "%s: gate is not aligned", fn);
@@ -290,12 +293,12 @@ int moe_norm_residual(const void *y, int dtype, int top_k, const void *residual,
   const char *fn = "moe_norm_residual";
   CHECK(check_norm(dtype, r_dtype, top_k, y, gate_kind, gate, M, N, fn));
   REQUIRE(eps >= 0.0f, MOE_EINVAL, "%s: eps=%g", fn, (double)eps);
+  if (M == 0) return ok();
   REQUIRE(y || residual, MOE_EINVAL, "%s: neither a block nor a residual", fn);
   REQUIRE(y || !(w_post || rstd_post), MOE_EINVAL, "%s: a norm after no block", fn);
   REQUIRE((w_pre == nullptr) == (h == nullptr), MOE_EINVAL, "%s: w_pre and h go together", fn);
   REQUIRE((w_post || !rstd_post) && (w_pre || !rstd_pre), MOE_EINVAL,
           "%s: the factor of a norm that is not taken", fn);
-  if (M == 0) return ok();
   REQUIRE(r, MOE_EINVAL, "%s: null pointer argument", fn);
   ALIGNED16(residual);
   ALIGNED16(w_post);
@@ -309,7 +312,9 @@ int moe_norm_residual(const void *y, int dtype, int top_k, const void *residual,
 }
 
 size_t moe_norm_backward_workspace_bytes(int M, int N) {
-  if (M < 1 || M > MOE_MAX_NORM_ROWS || N < 8 || N % 8 || N > MOE_MAX_NORM_COLUMNS) return 0;
+  if (M < 1 || M > MOE_MAX_NORM_ROWS || N < 8 || N % 8 || N > MOE_MAX_NORM_COLUMNS ||
+      (long long)M * N > MOE_MAX_NORM_VALUES)
+    return 0;
   return norm_backward_workspace_bytes(M, N);
 }
 
@@ -322,10 +327,10 @@ int moe_norm_residual_backward(const void *d_r, const void *d_h, const void *y, 
                                void *workspace, hipStream_t stream) {
   const char *fn = "moe_norm_residual_backward";
   CHECK(check_norm(dtype, r_dtype, top_k, y, gate_kind, gate, M, N, fn));
-  REQUIRE((w_pre == nullptr) == (d_h == nullptr), MOE_EINVAL, "%s: w_pre and d_h go together", fn);
-  REQUIRE(d_h || d_r, MOE_EINVAL, "%s: no gradient comes in", fn);
-  REQUIRE((y == nullptr) == (d_y == nullptr), MOE_EINVAL, "%s: y and d_y go together", fn);
-  REQUIRE(y || !w_post, MOE_EINVAL, "%s: a norm after no block", fn);
+  REQUIRE((w_pre == nullptr) == (d_h == nullptr) || M == 0, MOE_EINVAL, "%s: w_pre and d_h go together", fn);
+  REQUIRE(d_h || d_r || M == 0, MOE_EINVAL, "%s: no gradient comes in", fn);
+  REQUIRE((y == nullptr) == (d_y == nullptr) || M == 0, MOE_EINVAL, "%s: y and d_y go together", fn);
+  REQUIRE(y || !w_post || M == 0, MOE_EINVAL, "%s: a norm after no block", fn);
   REQUIRE((w_post || !d_w_post) && (w_pre || !d_w_pre) && (gate || !d_gate), MOE_EINVAL,
           "%s: the gradient of a weight or gate that is not there", fn);
   REQUIRE(!w_post || rstd_post || M == 0, MOE_EINVAL, "%s: null rstd_post", fn);

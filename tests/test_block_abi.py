@@ -212,6 +212,29 @@ def test_norm_backward_rejects(kw, code):
 
 
 @needs_lib
+@no_gpu
+def test_norms_refuse_more_values_than_a_launch_has_threads():
+    M, N = (1 << 35) // 4096 + 1, 4096
+    assert qm.MOE_MAX_NORM_VALUES == 1 << 35
+    assert qm.moe_norm_backward_workspace_bytes(M, N) == 0
+    assert qm.moe_norm_backward_workspace_bytes(M - 1, N) > 0
+    test_norm_rejects(dict(M=M, N=N, top_k=1), UNS)
+    test_norm_backward_rejects(dict(M=M, N=N, top_k=1), UNS)
+
+
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("gate_kind", [0, 1, 2])
+def test_norms_of_no_tokens_take_arrays_without_an_address(gate_kind):
+    gate = FAKE if gate_kind == 1 else None
+    assert qm.moe_norm_residual(None, 1, 2, None, 1, FAKE, gate, gate_kind, 1.0, 1.0, FAKE, 1e-6, 0,
+                                64, None, None, None, None, stream=0) == qm.MOE_OK
+    assert qm.moe_norm_residual_backward(None, None, None, 1, 2, None, 1, FAKE, gate, gate_kind, 1.0,
+                                         1.0, FAKE, None, None, 0, 64, None, None, None, None, None,
+                                         None, stream=0) == qm.MOE_OK
+
+
+@needs_lib
 def test_host_tensors_are_refused():
     import torch
     x = torch.zeros(16, 64, dtype=torch.bfloat16)

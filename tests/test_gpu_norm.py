@@ -234,6 +234,22 @@ def test_no_tokens():
         assert not bool(o.any())
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+def test_runner_of_no_tokens(gate):
+    N, t = 72, torch.bfloat16
+    norm = runner.BlockNorm(0, N, 2, gate=gate, train=True)
+    y, x = torch.empty(0, N, dtype=t, device=DEV), torch.empty(0, N, dtype=t, device=DEV)
+    w = torch.ones(N, device=DEV)
+    g = {"none": None, "channel": w, "token": torch.empty(0, device=DEV)}[gate]
+    for d in (norm.d_w_pre, norm.d_w_post, norm.d_gate):
+        d.fill_(7.0)
+    r, h = norm.forward(y, x, w, w, g)
+    assert tuple(r.shape) == tuple(h.shape) == (0, N)
+    _, _, d_pre, d_post, d_gate = norm.backward(x, x, y, w, w, g)
+    for d in (d_pre, d_post, d_gate):
+        assert d is None or not bool(d.any())
+
+
 def test_a_row_of_infinities_stays_a_row():
     c = Case(20, 264, 1, "bf16", "f32", True, "none")
     r, h, _, _ = c.forward()
