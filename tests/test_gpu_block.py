@@ -214,3 +214,21 @@ def test_grouped_products_of_a_captured_graph_follow_the_offsets(rows):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(bool(torch.isfinite(t.float()).all()) for t in got)
+
+
+def test_runners_of_no_rows_and_no_tokens():
+    t = torch.bfloat16
+    ffn = runner.GatedFFN(0, 72, 40, 3, train=True)
+    x = torch.empty(0, 72, dtype=t, device=DEV)
+    w_up, w_down = torch.ones(3, 80, 72, dtype=t, device=DEV), torch.ones(3, 72, 40, dtype=t, device=DEV)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    ffn.dw_up.fill_(7.0)
+    ffn.dw_down.fill_(7.0)
+    assert tuple(ffn.forward(x, w_up, w_down, off).shape) == (0, 72)
+    dx, dw_up, dw_down = ffn.backward(x, x, w_up, w_down, off)
+    assert tuple(dx.shape) == (0, 72) and not bool(dw_up.any()) and not bool(dw_down.any())
+    lora = runner.LoraAdapters(0, 72, 8, 2)
+    lora.plan(torch.empty(0, dtype=torch.int32, device=DEV))
+    a, b = torch.ones(2, 8, 72, dtype=t, device=DEV), torch.ones(2, 40, 8, dtype=t, device=DEV)
+    out = torch.empty(0, 40, dtype=t, device=DEV)
+    assert lora.add(x, a, b, out, out) is out
