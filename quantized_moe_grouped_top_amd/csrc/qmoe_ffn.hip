@@ -626,20 +626,25 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(const GroupedArgs p) {
 // One workgroup of four wavefronts per tile, T / 2 x T / 2 outputs each, for products
 // whose 256 x 256 tiles are fewer than the card has CUs.  Stages of 64 of the
 // contraction, copied kSlots - 1 ahead; one barrier a stage, behind which the slot read
-// last is free.  Short stages on many workgroups: what bounds it is the time from a
-// copy to its use, and the LDS (its reads take 1.5 (T = 128) or 3 times as long as the
-// products).
-template <typename Ty, int kLayout, int kEpi, int T>
-__global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
+// last is free.  Many tiles of 64 x 64 are bound by what the L2 gives (224 of them, depth
+// 3584: 9 TB/s), those of 128 by the LDS (its reads take 1.5 times as long as the products).
+// Few tiles are bound by the time of a stage, 0.3 us from a barrier to the next, whatever
+// the copies' lead (seven stages instead of three: 10 to 20% slower): there two groups of
+// four wavefronts take every other stage each and add their sums through LDS (130 rows, 8192
+// -> 512 back 40.5 us with one group, 29.9 with two; 128 rows, 4096 -> 2 x 512 19.2,
+// 15.6; but 256 tiles, 256 x 2048 -> 4096 back, 14.1, 14.8).
+template <typename Ty, int kLayout, int kEpi, int T, int kGroups = 1>
+__global__ __launch_bounds__(256 * kGroups, 2) void square_kernel(const GroupedArgs p) {
   constexpr bool kRT = kLayout == kWgrad, kCT = kLayout != kLinear;
   constexpr int kSlots = T == 64 ? 4 : 2;
   constexpr int kPart = T * 128, kSlot = 2 * kPart, kRowB = 2 * T;
   constexpr int P = T / 32;                           // copies of a wavefront, stage and operand
   constexpr int F = T / 32;                           // fragments of a wavefront either way
-  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kSlots * kSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kGroups * kSlots * kSlot];
+  __shared__ f32x4 s_part[kGroups == 1 ? 1 : F * F * 256];
   __shared__ Segments s_seg;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, group = __builtin_amdgcn_readfirstlane(tid >> 8);
   const int wm = wave >> 1, wn = wave & 1;
   const int g = lane >> 4, r16 = lane & 15;
   constexpr int kTN = kEpi == kGatedUp ? T / 2 : T;
@@ -649,7 +654,7 @@ __global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
                 [&](int n) { return (kLayout == kWgrad ? ntr : (n + T - 1) / T) * ntn; },
                 [](int) { return 1.0f; });
   const int total = __builtin_amdgcn_readfirstlane(s_seg.first[kMaxExperts]);
-  const uint32_t ring = lds_addr(s_ring);
+  const uint32_t ring = lds_addr(s_ring) + (uint32_t)(group * kSlots * kSlot);
   auto swz = [](int r) QMOE_INLINE { return (r >> 1) & 7; };
   // 32-byte granules of an LDS row across: 16 of them for T = 256, 4 for T = 64, whose rows
   // of 128 bytes take two of k into each 256 bytes of banks
@@ -682,7 +687,7 @@ __global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
     // rows fastest: the workgroups of a column tile share its columns
     const int ntm = kLayout == kWgrad ? ntr : (n + T - 1) / T;
     const int tn = local / ntm, m0 = (local - tn * ntm) * T, n0 = tn * kTN;
-    const int stages = (depth + 63) >> 6;
+    const int stages = (depth + 64 * kGroups - 1) / (64 * kGroups);      // of a group
 
     const uint16_t *r_src = kRT ? p.r + lo * p.ldr + m0 : p.r + (lo + m0) * p.ldr;
     const uint16_t *c_src = kLayout == kWgrad ? p.c + lo * p.ldc + n0
@@ -714,14 +719,14 @@ __global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
     // copies in flight stay the same
     auto copy_stage = [&](int s) QMOE_INLINE {
       const uint32_t at = ring + (uint32_t)((s & (kSlots - 1)) * kSlot + P * wave * 1024);
-      const int left = depth - 64 * s;
+      const int from = s * kGroups + group, left = depth - 64 * from;
 #pragma unroll
       for (int u = 0; u < P; ++u)
-        dma16z(r_src + s * r_step, r_k[u] < left ? r_off[u] : kOut, at + u * 1024);
+        dma16z(r_src + from * r_step, r_k[u] < left ? r_off[u] : kOut, at + u * 1024);
 #pragma unroll
       for (int u = 0; u < P; ++u) {
         const bool second = kEpi == kGatedUp && ((P * wave + u) >> 1 & 1);      // rows 16 .. 31 of 32
-        dma16z(c_src + s * c_step + (second ? (long long)p.H * p.ldc : 0), c_k[u] < left ? c_off[u] : kOut,
+        dma16z(c_src + from * c_step + (second ? (long long)p.H * p.ldc : 0), c_k[u] < left ? c_off[u] : kOut,
                at + kPart + u * 1024);
       }
     };
@@ -755,6 +760,21 @@ __global__ __launch_bounds__(256, 2) void square_kernel(const GroupedArgs p) {
 #pragma unroll
           for (int i = 0; i < F; ++i) acc[i][j] = mfma16<Ty>(fc[j], fr[i], acc[i][j]);
       }
+    }
+    if constexpr (kGroups == 2) {
+      f32x4 *const part = s_part + (tid & 255);
+      if (group == 1) {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j) part[256 * (i * F + j)] = acc[i][j];
+      }
+      __syncthreads();
+      if (group == 1) continue;
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] += part[256 * (i * F + j)];
     }
     store_tile<Ty, kLayout, kEpi, F, F>(p, e, kLayout == kWgrad ? 0 : lo, m0 + wm * (T / 2), nrow,
                                         n0 + wn * (kTN / 2), acc);
@@ -937,6 +957,8 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((wide_kernel<Ty, kLayout, kEpi, 256>), dim3(kCus), block, 0, s, a);
   } else if (tiles(128) >= 192) {
     hipLaunchKernelGGL((square_kernel<Ty, kLayout, kEpi, 128>), dim3(2 * kCus), block, 0, s, a);
+  } else if (tiles(64) <= kCus / 2) {
+    hipLaunchKernelGGL((square_kernel<Ty, kLayout, kEpi, 64, 2>), dim3(kCus), dim3(512), 0, s, a);
   } else {
     hipLaunchKernelGGL((square_kernel<Ty, kLayout, kEpi, 64>), dim3(2 * kCus), block, 0, s, a);
   }
