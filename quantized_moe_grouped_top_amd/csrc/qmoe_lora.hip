@@ -197,7 +197,7 @@ template <typename Ty, typename Out, int S>
 __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kernel(const LoraArgs p, int splits, int blocks) {
   typedef typename Out::T T;
   constexpr int kRow = 32 * S + 8;                    // 16-bit values of an LDS row: off the banks
-  // two parts leave out 2^-16 of v, or for float32 results three less than its own rounding
+  // two parts leave out 2^-16 of v (bf16; fp16 2^-22), three 2^-24, float32's own rounding
   constexpr int kParts = sizeof(T) == 4 ? 3 : 2;
   __shared__ __attribute__((aligned(16))) uint16_t s_v[kParts][kTokens][kRow];
   __shared__ float s_up[kTokens];
@@ -282,8 +282,10 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
       }
   }
   for (int m0 = 0; m0 < p.block_m; m0 += tokens) {
-    // v in 16-bit parts; for fp16 through a power of two that brings a token's largest
-    // value near 1, so that the parts of every value lie in its range
+    // v in 16-bit parts; for fp16 through a power of two that brings a token's largest value to
+    // 2^14 .. 2^15.  Below that fp16 ends at steps of 2^-24, so that beside the parts' own
+    // 2^-39 of the largest value is left out at most: parts around 1 would leave out 2^-25 of
+    // it, which is all of a value that far below, and more than 2^-16 of any below 2^-9.
     float top = 0.0f, down = scale, up = 1.0f;
 #pragma unroll
     for (int i = 0; i < kQuads; ++i)
@@ -298,8 +300,8 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
       up = scale;
       if (top > 0.0f && top < __builtin_inff()) {
         const int e = min(max(ilogbf(top), -100), 100);
-        down = ldexpf(1.0f, -e);
-        up = ldexpf(scale, e);
+        down = ldexpf(1.0f, 14 - e);
+        up = ldexpf(scale, e - 14);
       }
     }
 #pragma unroll

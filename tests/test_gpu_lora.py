@@ -189,3 +189,55 @@ def test_a_plan_for_more_features_serves_fewer():
     with pytest.raises(AssertionError):
         small.add(torch.zeros(9, 512, dtype=torch.bfloat16, device=DEV),
                   torch.zeros(4, 16, 512, dtype=torch.bfloat16, device=DEV), c.b, a)
+
+
+def _split_case(dtype, out, below, T=24, R=16, N=128):
+    """One adapter whose inner vector is known to the bit: v of rank r is an integer of
+    24 bits times 2^(4 - below[r]) (a product of two full values and one of two small
+    ones behind it), b has one power of two a column, scale is one: whatever is missing
+    in the result was left out of v."""
+    c = Case(T, 8, N, R, 1, dtype, out, 16, 0, ranks=False)
+    bits = {"bf16": 8, "f16": 11}[dtype]
+    g = _rng(dtype, out, tuple(below))
+    lo, hi, small = 2 ** (bits - 1), 2 ** bits, {"bf16": 15, "f16": 1}[dtype]
+    shift = 24 - 2 * bits                       # the second product stands that far behind
+    big = torch.randint(lo, hi, (T,), generator=g).double()
+    add = torch.randint(1, small + 1, (T,), generator=g).double()
+    a0 = torch.randint(lo, hi, (R,), generator=g).double()
+    a1 = 2.0 * torch.randint(0, 2 if dtype == "f16" else 8, (R,), generator=g).double() + 1.0
+    unit = 2.0 ** (4 - torch.tensor([below[r % len(below)] for r in range(R)], dtype=torch.double))
+    t = DT[dtype][1]
+    x, a = torch.zeros(T, 8, dtype=torch.double), torch.zeros(R, 8, dtype=torch.double)
+    x[:, 2], x[:, 5] = big, add
+    a[:, 2], a[:, 5] = a0 * unit, a1 * unit * 2.0 ** -shift
+    b = torch.zeros(N, R, dtype=torch.double)
+    n = torch.arange(N)
+    b[n, n % R] = 2.0 ** torch.randint(-2, 3, (N,), generator=g).double() * torch.where(n % 3 == 0, -1.0, 1.0)
+    for v in (x, a, b):
+        assert torch.equal(v, v.to(t).double())
+    v = x @ a.t()
+    assert torch.equal(v, v.float().double())
+    c.x[:, :8], c.a[0], c.b[0] = x.to(t).to(DEV), a.to(t).to(DEV), b.to(t).to(DEV)
+    scale = 2.0 ** {"bf16": -8, "f16": -14}[dtype]          # results in fp16's normal range
+    c.scales[0] = scale
+    return c, v.numpy(), (b * scale).numpy()
+
+
+@pytest.mark.parametrize("below", [(0, 0, 1, 3), (0, 10, 6, 12), (0, 14, 16, 15), (0, 18, 20, 17)], ids=str)
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
+                                       ("bf16", "f16")])
+def test_what_is_left_out_of_the_inner_vector(dtype, out, below):
+    """Two 16-bit parts leave out 2^-16 of a value of the inner vector (two steps of a
+    half, bf16), three 2^-24 of it; in fp16 values reach down to 2^-39 of the token's
+    largest besides: that is brought to 2^14 at least, where the smallest step of fp16
+    is 2^-24 and half of it 2^-39 of 2^14.  No sum is in the way: every column has one
+    product.  Then half a step of the output's type."""
+    c, v, b = _split_case(dtype, out, below)
+    left = (2.0 ** -24 if out == "f32" else 2.0 ** -16) * np.abs(v)
+    if dtype == "f16":
+        left += 2.0 ** -39 * np.abs(v).max(1, keepdims=True)
+    ref, err = v @ b.T, left @ np.abs(b).T
+    got = _np(c.run(addend=False))
+    tol = err + HALF[out] * (np.abs(ref) + err)
+    worst = np.max(np.abs(got - ref) / tol)
+    assert worst <= 1.0, worst
