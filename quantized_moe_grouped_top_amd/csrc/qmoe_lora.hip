@@ -285,20 +285,21 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
     // v in 16-bit parts; for fp16 through a power of two that brings a token's largest value to
     // 2^14 .. 2^15.  Below that fp16 ends at steps of 2^-24, so that beside the parts' own
     // 2^-39 of the largest value is left out at most: parts around 1 would leave out 2^-25 of
-    // it, which is all of a value that far below, and more than 2^-16 of any below 2^-9.
+    // it, which is all of a value that far below, and more than 2^-16 of any below 2^-9.  An
+    // infinity stays one in any case: the largest finite value counts.
     float top = 0.0f, down = scale, up = 1.0f;
 #pragma unroll
     for (int i = 0; i < kQuads; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (4 * (part + i * each) + q >= rank) v[i][q] = 0.0f;
-        top = fmaxf(top, fabsf(v[i][q]));
+        top = fmaxf(top, __builtin_isfinite(v[i][q]) ? fabsf(v[i][q]) : 0.0f);
       }
     if constexpr (std::is_same<Ty, TypeF16>::value) {
       for (int d = 1; d < each; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
       down = 1.0f;
       up = scale;
-      if (top > 0.0f && top < __builtin_inff()) {
+      if (top > 0.0f) {
         const int e = min(max(ilogbf(top), -100), 100);
         down = ldexpf(1.0f, 14 - e);
         up = ldexpf(scale, e - 14);

@@ -241,3 +241,15 @@ def test_what_is_left_out_of_the_inner_vector(dtype, out, below):
     tol = err + HALF[out] * (np.abs(ref) + err)
     worst = np.max(np.abs(got - ref) / tol)
     assert worst <= 1.0, worst
+
+
+def test_an_infinite_value_of_the_inner_vector_beside_large_ones_in_fp16():
+    """inf b0 + 10^6 b1: an infinity of b0's sign, whatever sign b1 has."""
+    c = Case(20, 8, 64, 16, 1, "f16", "f32", 16, 0, ranks=False, scales=False)
+    c.x[:, :8] = 1000.0
+    c.a[0].fill_(125.0)                          # v = 10^6, above fp16's largest value
+    c.a[0, 3, 2] = float("inf")
+    c.b[0] = torch.where(torch.rand(64, 16, generator=_rng("signs")) < 0.5, -1.0, 1.0).half().to(DEV)
+    got = c.run(addend=False)
+    want = c.b[0, :, 3].float() * float("inf")
+    assert torch.equal(got, want.expand(20, 64))
