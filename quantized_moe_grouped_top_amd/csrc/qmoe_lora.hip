@@ -185,6 +185,17 @@ __device__ __forceinline__ void store8(typename Out::T *at, const float (&f)[8])
   }
 }
 
+// The 16-bit pairs of v with infinities and NaN as 0.
+template <typename Ty>
+__device__ __forceinline__ i32x4 finite_only(const i32x4 &v) {
+  constexpr int kExp = std::is_same<Ty, TypeBf16>::value ? 0x7F80 : 0x7C00;     // all ones in those
+  i32x4 o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    o[q] = v[q] & ((v[q] & kExp) == kExp ? ~0xFFFF : -1) & ((v[q] >> 16 & kExp) == kExp ? 0xFFFF : -1);
+  return o;
+}
+
 // One workgroup per block of tokens and 512 columns, 64 a wavefront, neighbouring workgroups
 // neighbouring columns: 1 KB of a token's row together (4096 tokens, 28672 columns, rank 64:
 // 127 us, with 256 columns 139, neighbours in tokens 160; sums split by every wavefront for
@@ -354,18 +365,36 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
         fetch_add();
       }
       f32x4 acc[4];
+      auto products = [&](auto clean) QMOE_INLINE {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        if (32 * s >= rank) break;
+        for (int s = 0; s < S; ++s) {
+          if (32 * s >= rank) break;
 #pragma unroll
-        for (int k = kParts - 1; k >= 0; --k) {       // the smallest first
-          const i32x4 w = *reinterpret_cast<const i32x4 *>(&s_v[k][m + r16][32 * s + 8 * g]);
+          for (int k = kParts - 1; k >= 0; --k) {     // the smallest first
+            const i32x4 w = *reinterpret_cast<const i32x4 *>(&s_v[k][m + r16][32 * s + 8 * g]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mfma16<Ty>(bv[j][s], w, acc[j]);
+            for (int j = 0; j < 4; ++j) {
+              i32x4 b = bv[j][s];
+              if constexpr (decltype(clean)::value)
+                if (k > 0) {
+                  asm volatile("" : "+v"(b));         // cleaned here each time, not held beside B
+                  b = finite_only<Ty>(b);
+                }
+              acc[j] = mfma16<Ty>(b, w, acc[j]);
+            }
+          }
         }
-      }
+      };
+      products(std::false_type{});
+      // An infinity of B belongs to the first part of v alone: the others may be 0 or of the
+      // other sign, and with theirs its sum has become NaN.
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        nan |= __builtin_isunordered(acc[j][0], acc[j][1]) | __builtin_isunordered(acc[j][2], acc[j][3]);
+      if (__ballot(nan) != 0) products(std::true_type{});
       const float by = s_up[m + r16];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {

@@ -253,3 +253,37 @@ def test_an_infinite_value_of_the_inner_vector_beside_large_ones_in_fp16():
     got = c.run(addend=False)
     want = c.b[0, :, 3].float() * float("inf")
     assert torch.equal(got, want.expand(20, 64))
+
+
+@pytest.mark.parametrize("dtype,out,R", [("bf16", "bf16", 16), ("bf16", "f32", 64), ("f16", "f16", 128),
+                                         ("f16", "f32", 24)])
+def test_infinite_values_of_b(dtype, out, R):
+    """v inf is an infinity of v's sign, also where v's later parts are 0 or of the other
+    sign (v = 1, 1 - 2^-9 and such), NaN where v is 0; a NaN stays in its column."""
+    T, N, rank = 40, 200, R - 3
+    c = Case(T, 8, N, R, 2, dtype, out, 16, 1, ranks=False, scales=False)
+    c.ranks = torch.tensor([R, rank], dtype=torch.int32, device=DEV)
+    g = _rng("inf b", dtype, out)
+    # x a: sums of a power of two and a small one either side of it; the last two tokens 0
+    c.x[:, :8] = 0.0
+    c.x[:T - 2, 0] = 1.0
+    c.x[:T - 2, 1] = torch.tensor([0.0, 2.0 ** -9, -2.0 ** -9, 2.0 ** -13])[torch.arange(T - 2) % 4].to(DEV)
+    sign = torch.where(torch.rand(R, generator=g) < 0.5, -1.0, 1.0)
+    c.a[1, :, 0] = sign.to(DEV)
+    c.a[1, :, 1] = 1.0
+    c.b[1, 7, 3] = c.b[1, 150, rank - 1] = float("inf")
+    c.b[1, 64, 0] = float("-inf")
+    c.b[1, 65, 5], c.b[1, 65, 6] = sign[5] * float("inf"), sign[6] * float("inf")
+    c.b[1, 199, 1] = float("nan")
+    c.b[1, :, rank:] = float("inf")                       # past the rank: not used
+    c.b[0] = float("inf")                                 # nobody's
+    got = c.run(addend=True).double().cpu()
+    n, m = torch.tensor([7, 150, 64, 65]), T - 2
+    inf = float("inf")
+    want = torch.stack([sign[3], sign[rank - 1], -sign[0], torch.ones(())]).double() * inf
+    assert torch.equal(got[:m, n], want.expand(m, 4))
+    assert bool(torch.isnan(got[m:, n]).all()) and bool(torch.isnan(got[:, 199]).all())
+    rest = [i for i in range(N) if i not in (7, 150, 64, 65, 199)]
+    c.b[1, [7, 150, 64, 65, 199]] = 0.0
+    finite = c.run(addend=True).double().cpu()
+    assert bool(torch.isfinite(finite).all()) and torch.equal(got[:, rest], finite[:, rest])
