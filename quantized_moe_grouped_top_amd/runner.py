@@ -478,8 +478,10 @@ class RoutedMoE:
         routed experts' sum.  `norm` = (BlockNorm, residual, w_pre, w_post, gate):
         the norm after the layer, gate, residual and next norm, and their (r, h) is
         returned; without a shared expert (top_k of the BlockNorm that of the layer)
-        it takes the place of the combine, with one (top_k 1) it follows the sum."""
+        it takes the place of the combine, with one (top_k 1) it follows the sum.
+        A layer that holds part of the experts takes no norm: it needs the sum of all."""
         if norm is not None:
+            assert self.router is None or self.router.holds_all
             block, norm_args = norm[0], norm[1:]
             assert (block.M, block.N, block.dtype) == (self.M, self.N, MOE_BF16)
             assert block.top_k == (1 if shared is not None else self.top_k)

@@ -242,6 +242,34 @@ def test_host_tensors_are_refused():
         qm.moe_grouped_linear(x, 64, x, 1, None, 16, 64, 16, 1, x, 64)
 
 
+@needs_lib
+@no_gpu
+@pytest.mark.parametrize("shared", [False, True])
+def test_layer_refuses_a_norm_of_part_of_the_experts(monkeypatch, shared):
+    """A norm of some of the experts' results is no part of the norm of all of them,
+    and the residual would be added by every holder of a window."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = []
+    for name in ("moe_route_topk", "moe_align_topk_ids", "moe_quantize_act", "moe_grouped_gemm_int8w8a8",
+                 "moe_combine", "moe_gemm_int8w8a8", "moe_norm_residual"):
+        monkeypatch.setattr(runner, name, lambda *a, name=name: calls.append(name))
+    x, logits = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(4, 8)
+    w, s = torch.zeros(8, 32, 32, dtype=torch.int8), torch.zeros(8, 32)
+    block = runner.BlockNorm(4, 32, 1 if shared else 2, device="cpu")
+    sh = (runner.Int8Linear(4, 32, 32, device="cpu"), w[0], s[0]) if shared else None
+    for first, n_local in ((0, 4), (4, 4), (6, 4)):
+        r = runner.TopKRouter(4, 8, 2, expert_first=first, n_local=n_local, device="cpu")
+        moe = runner.RoutedMoE("int8dq", 4, 32, 32, n_local, 2, device="cpu", router=r)
+        with pytest.raises(AssertionError):
+            moe.forward(x, logits, w[:4], s[:4], shared=sh, norm=(block, x, s[0], None, None))
+    assert not calls
+    r = runner.TopKRouter(4, 8, 2, device="cpu")
+    moe = runner.RoutedMoE("int8dq", 4, 32, 32, 8, 2, device="cpu", router=r)
+    moe.forward(x, logits, w, s, shared=sh, norm=(block, x, s[0], None, None))
+    assert calls[-1] == "moe_norm_residual" and ("moe_combine" in calls) == shared
+
+
 # ---- the reference ------------------------------------------------------------------
 def test_activations():
     g = np.linspace(-12, 12, 97)
