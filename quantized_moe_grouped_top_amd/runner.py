@@ -202,7 +202,7 @@ class Int8Linear:
         taken of the unquantized x, is added to the product."""
         if lora is not None:
             adapters, a, b, scales, ranks = lora
-            assert adapters.T == self.M and x.dtype == adapters.torch_dtype
+            assert adapters.T == self.M and adapters.dtype == MOE_BF16
             adapters.check(x, a, b, self.out if out is None else out, scales, ranks)
         self.quantize(x)
         out = self.gemm(w_q, w_scale, bias, addend, out)
@@ -215,7 +215,11 @@ class LoraAdapters:
     """Low-rank adapters of many requests beside shared projections: T tokens, L
     adapters of rank R at most, inputs of K features at most.  `plan` groups the
     tokens by adapter, once for all projections of a step; `add` adds
-    scales[a] b[a] (a[a] x_t) to a projection's output."""
+    scales[a] b[a] (a[a] x_t) to a projection's output (int16: the bits of bf16
+    values)."""
+
+    _OUT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16,
+            torch.int16: MOE_BF16}
 
     def __init__(self, T, K, R, L, dtype="bf16", block_m=None, device="cuda"):
         self.T, self.K, self.R, self.L = T, K, R, L
@@ -239,11 +243,13 @@ class LoraAdapters:
 
     def check(self, x, a, b, out, scales=None, ranks=None):
         K, N = a.shape[2], b.shape[1]
-        assert x.dtype == self.torch_dtype and tuple(x.shape) == (self.T, K) and K <= self.K
-        assert x.stride(1) == 1
+        # the bits of bf16 values may come as 16-bit integers
+        assert x.dtype == self.torch_dtype or (self.dtype == MOE_BF16 and
+                                               x.dtype in (torch.int16, torch.uint16))
+        assert tuple(x.shape) == (self.T, K) and K <= self.K and x.stride(1) == 1
         assert _rows_of(a, self.torch_dtype, (self.L, self.R, K))
         assert _rows_of(b, self.torch_dtype, (self.L, N, self.R))
-        assert tuple(out.shape) == (self.T, N) and out.stride(1) == 1
+        assert tuple(out.shape) == (self.T, N) and out.stride(1) == 1 and out.dtype in self._OUT
         assert scales is None or _rows_of(scales, torch.float32, (self.L,))
         assert ranks is None or _rows_of(ranks, torch.int32, (self.L,))
 
@@ -252,12 +258,12 @@ class LoraAdapters:
         self.check(x, a, b, out, scales, ranks)
         assert addend is None or (addend.dtype == out.dtype and addend.shape == out.shape and
                                   addend.stride() == out.stride())
-        code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[out.dtype]
         # a workspace for K features holds that of fewer
         K, N = a.shape[2], b.shape[1]
         moe_lora_add(x, x.stride(0), a, b, ranks, scales, self.dtype, self.adapter_ids,
                      self.sorted_token_ids, self.expert_ids, self.num_tokens_post_padded, self.T, K,
-                     N, self.R, self.L, self.block_m, addend, code, out, out.stride(0), self.ws)
+                     N, self.R, self.L, self.block_m, addend, self._OUT[out.dtype], out,
+                     out.stride(0), self.ws)
         return out
 
 

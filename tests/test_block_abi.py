@@ -270,6 +270,40 @@ def test_layer_refuses_a_norm_of_part_of_the_experts(monkeypatch, shared):
     assert calls[-1] == "moe_norm_residual" and ("moe_combine" in calls) == shared
 
 
+@needs_lib
+@no_gpu
+def test_linear_refuses_adapters_for_another_output_before_the_product(monkeypatch):
+    """The bits of bf16 values may come as int16, in the adapters as in the product;
+    any other type is refused before anything is enqueued."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = []
+    for name in ("moe_quantize_act", "moe_gemm_int8w8a8", "moe_lora_add"):
+        monkeypatch.setattr(runner, name, lambda *a, name=name: calls.append((name, a)))
+    lin = runner.Int8Linear(4, 32, 16, device="cpu")
+    ad = runner.LoraAdapters(4, 32, 8, 2, device="cpu")
+    bf = torch.bfloat16
+    x, out = torch.zeros(4, 32, dtype=bf), torch.zeros(4, 16, dtype=bf)
+    a, b = torch.zeros(2, 8, 32, dtype=bf), torch.zeros(2, 16, 8, dtype=bf)
+    w, s = torch.zeros(16, 32, dtype=torch.int8), torch.zeros(16)
+    for bad in (out.double(), out.int(), out.to(torch.uint8)):
+        with pytest.raises(AssertionError):
+            lin.forward(x, w, s, out=bad, lora=(ad, a, b, None, None))
+        with pytest.raises(AssertionError):
+            ad.add(x, a, b, bad, bad)
+    half = runner.LoraAdapters(4, 32, 8, 2, dtype="f16", device="cpu")
+    with pytest.raises(AssertionError):
+        half.add(x.view(torch.int16), a.half(), b.half(), out)
+    assert not calls
+    for xs in (x, x.view(torch.int16)):
+        for o in (out, out.view(torch.int16)):
+            assert lin.forward(xs, w, s, out=o, lora=(ad, a, b, None, None)) is o
+            (quantize, _), (gemm, _), (add, args) = calls
+            assert (quantize, gemm, add) == ("moe_quantize_act", "moe_gemm_int8w8a8", "moe_lora_add")
+            assert args[0] is xs and args[18] == qm.MOE_BF16 and args[17] is o and args[19] is o
+            calls.clear()
+
+
 # ---- the reference ------------------------------------------------------------------
 def test_activations():
     g = np.linspace(-12, 12, 97)

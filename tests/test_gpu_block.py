@@ -232,3 +232,28 @@ def test_runners_of_no_rows_and_no_tokens():
     a, b = torch.ones(2, 8, 72, dtype=t, device=DEV), torch.ones(2, 40, 8, dtype=t, device=DEV)
     out = torch.empty(0, 40, dtype=t, device=DEV)
     assert lora.add(x, a, b, out, out) is out
+
+
+def test_shared_expert_with_adapters_on_the_layers_sum():
+    """The layer's sum is the bits of bf16 values; a shared expert with the adapters of
+    the tokens' requests is added to it where it lies, and the norm follows."""
+    run, moe, first, last, (x, w_pre, w_next, w_post, gate) = _layer(True)
+    g = _gen(21)
+    rnd = lambda *s, m=1.0: (torch.randn(*s, generator=g, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    w_q, w_s = runner.quantize_weights(rnd(E, K, K, m=K ** -0.5).float(), "int8dq")
+    sh_q, sh_s = runner.quantize_weights(rnd(1, K, K, m=K ** -0.5).float(), "int8")
+    lin, ad = runner.Int8Linear(M, K, K), runner.LoraAdapters(M, K, 16, 3)
+    ad.plan(torch.arange(M, dtype=torch.int32, device=DEV) % 4 - 1)      # a quarter without
+    a, b = rnd(3, 16, K, m=K ** -0.5), rnd(3, K, 16)
+    logits = rnd(M, E).float()
+    total = moe.forward(x, logits, w_q, w_s)
+    want = total.view(torch.bfloat16).clone()
+    lin.forward(x, sh_q[0], sh_s[0], addend=want, out=want)
+    before = want.clone()
+    ad.add(x, a, b, want, want)
+    got = lin.forward(x, sh_q[0], sh_s[0], addend=total, out=total, lora=(ad, a, b, None, None))
+    assert got is total and torch.equal(got.view(torch.bfloat16), want)
+    assert torch.equal(want[::4], before[::4]) and not torch.equal(want, before)
+    r, h = (t.clone() for t in last.forward(total, x, w_next, w_post, gate))
+    again = last.forward(want, x, w_next, w_post, gate)
+    assert torch.equal(r, again[0]) and torch.equal(h, again[1])
