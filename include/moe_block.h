@@ -69,7 +69,9 @@ int moe_grouped_linear(const void *x, long long ldx, const void *w, int dtype,
 
 /* Gradient of y = h w[e]^T, h = act(g) * u, with respect to g and u:
  *     dh = dy w[e],  dg = dh u act'(g),  du = dh act(g)
- * dh stays unrounded and is not stored.
+ * dh stays unrounded and is not stored.  For an infinite g (one that left the
+ * type's range in moe_gated_up) act and act' are their limits: 0 and 0 at -inf, inf
+ * and 1 at inf.
  *   dy [rows, N], rows lddy apart;  w [E, N, H];  gu [rows, 2H]
  *   dgu [rows, 2H] = [dg | du]; may be gu itself
  *   h [rows, H], act(g) * u once more for w's gradient; or NULL */

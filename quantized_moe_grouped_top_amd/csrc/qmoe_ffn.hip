@@ -28,6 +28,8 @@ __device__ __forceinline__ float act_value(float g, int act) {
   }
   return g / (1.0f + __expf(-z));
 }
+// The gradient's g is the stored one, infinite where it left its type's range on the way
+// forward: there act and act' are their limits, 0 and 0, an infinity and 1.
 __device__ __forceinline__ void act_both(float g, int act, float &a, float &da) {
   float z = g, dz = 1.0f;
   if (act != MOE_GATED_SILU) {
@@ -36,8 +38,8 @@ __device__ __forceinline__ void act_both(float g, int act, float &a, float &da) 
     dz = 1.5957691216057308f * (1.0f + 3.0f * 0.044715f * gc * gc);
   }
   const float s = 1.0f / (1.0f + __expf(-z));
-  a = g * s;
-  da = s + a * (1.0f - s) * dz;
+  a = __builtin_elementwise_maximum(g, -__FLT_MAX__) * s;             // (these keep a NaN)
+  da = s + __builtin_elementwise_minimum(a, __FLT_MAX__) * (1.0f - s) * dz;
 }
 
 #define QMOE_INLINE __attribute__((always_inline))

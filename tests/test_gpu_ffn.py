@@ -381,3 +381,49 @@ def test_results_repeat():
         if first is None:
             first = out
         assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradient_at_infinite_gates(dtype, act):
+    """A gate that left its type's range on the way forward: act and act' have their
+    limits there (0 and 0; an infinity and 1); a NaN stays one."""
+    rows, N, H = 70, 72, 136
+    g = _rng("infinite gates", dtype, act)
+    w = _weights(1, N, H, dtype, g)
+    dy, gu = _rows((rows, N), dtype, g), _rows((rows, 2 * H), dtype, g)
+    inf = float("inf")
+    gu[:, 3], gu[:, 60], gu[:, 135] = -inf, inf, float("nan")
+    u = _np(gu)[:, H:]
+    dgu, h = _out(rows, 2 * H, dtype), _out(rows, H, dtype)
+    qm.moe_gated_down_backward(dy, N, w, gu, DT[dtype][0], None, rows, N, H, 1, ACT[act], dgu, h)
+    dg, du, h = dgu[:rows, :H], dgu[:rows, H:], h[:rows]
+    assert not bool(dg[:, 3].any()) and not bool(du[:, 3].any()) and not bool(h[:, 3].any())
+    dn, wn = _np(dy), _np(w)[0]
+    dh, mag = dn @ wn, np.abs(dn) @ np.abs(wn)
+    _close(dg[:, 60], dh[:, 60] * u[:, 60], N * U * (mag[:, 60] * np.abs(u[:, 60])), dtype, "dg")
+    assert np.array_equal(du[:, 60].double().cpu().numpy(), np.sign(dh[:, 60]) * inf)
+    assert np.array_equal(h[:, 60].double().cpu().numpy(), np.sign(u[:, 60]) * inf)
+    for t in (dg, du, h):
+        assert bool(torch.isnan(t[:, 135]).all())
+        rest = [i for i in range(H) if i not in (3, 60, 135)]
+        assert bool(torch.isfinite(t[:, rest]).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_past_a_gate_below_fp16(act):
+    """One token's gate of -80000 is -inf in fp16's gu and its h is 0: it adds nothing,
+    neither to its own gradient nor to the weights' (these in float32: the token's other
+    gates, 266 * 400 in float64, are above fp16's 65504)."""
+    rows, K, H = 40, 72, 40
+    g = _rng("below", act)
+    ffn = runner.GatedFFN(rows, K, H, 1, "f16", act, train=True, dw="f32")
+    x, dy = _rows((rows, K), "f16", g), _rows((rows, K), "f16", g)
+    w_up, w_down = _weights(1, 2 * H, K, "f16", g), _weights(1, K, H, "f16", g)
+    x[:, 0], x[7, 0] = 0.0, 400.0
+    w_up[0, 9, 0] = -200.0
+    y = ffn.forward(x, w_up, w_down).clone()
+    assert float(ffn.gu[7, 9]) == -float("inf") and float(ffn.h[7, 9]) == 0.0
+    grads = [t.clone() for t in ffn.backward(dy, x, w_up, w_down)]
+    assert all(bool(torch.isfinite(t).all()) for t in [y] + grads)
+    assert float(ffn.dgu[7, 9]) == 0.0 and float(ffn.dgu[7, H + 9]) == 0.0
