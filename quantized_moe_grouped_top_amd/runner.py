@@ -110,6 +110,12 @@ def _rows_of(t, dtype, shape):
     return t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()
 
 
+def _row_distance(t):
+    """Elements from a row of t to the next; of a single row its length, whatever
+    stride it has."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 class TopKRouter:
     """General router of fixed (M, E, top_k): softmax or sigmoid scores, an
     optional balance bias, groups, renormalised weights.  `route` fills
@@ -257,13 +263,14 @@ class LoraAdapters:
         """out = addend + the adapters' part; `addend` may be out (or None: 0)."""
         self.check(x, a, b, out, scales, ranks)
         assert addend is None or (addend.dtype == out.dtype and addend.shape == out.shape and
-                                  addend.stride() == out.stride())
+                                  addend.stride(1) == 1 and
+                                  _row_distance(addend) == _row_distance(out))
         # a workspace for K features holds that of fewer
         K, N = a.shape[2], b.shape[1]
-        moe_lora_add(x, x.stride(0), a, b, ranks, scales, self.dtype, self.adapter_ids,
+        moe_lora_add(x, _row_distance(x), a, b, ranks, scales, self.dtype, self.adapter_ids,
                      self.sorted_token_ids, self.expert_ids, self.num_tokens_post_padded, self.T, K,
                      N, self.R, self.L, self.block_m, addend, self._OUT[out.dtype], out,
-                     out.stride(0), self.ws)
+                     _row_distance(out), self.ws)
         return out
 
 
@@ -299,7 +306,7 @@ class GatedFFN:
 
     def forward(self, x, w_up, w_down, m_offsets=None):
         self._check(x, w_up, w_down, m_offsets)
-        moe_gated_up(x, x.stride(0), w_up, self.dtype, m_offsets, self.rows, self.K, self.H, self.E,
+        moe_gated_up(x, _row_distance(x), w_up, self.dtype, m_offsets, self.rows, self.K, self.H, self.E,
                      self.act, self.gu, self.h)
         moe_grouped_linear(self.h, self.H, w_down, self.dtype, m_offsets, self.rows, self.H, self.K,
                            self.E, self.y, self.K)
@@ -313,12 +320,12 @@ class GatedFFN:
         assert dy.stride(1) == 1
         rows, K, H, E, t = self.rows, self.K, self.H, self.E, self.dtype
         # h is there from the forward pass
-        moe_gated_down_backward(dy, dy.stride(0), w_down, self.gu, t, m_offsets, rows, K, H, E,
+        moe_gated_down_backward(dy, _row_distance(dy), w_down, self.gu, t, m_offsets, rows, K, H, E,
                                 self.act, self.dgu, None)
         moe_grouped_linear_dgrad(self.dgu, 2 * H, w_up, t, m_offsets, rows, K, 2 * H, E, self.dx, K)
-        moe_grouped_linear_wgrad(self.dgu, 2 * H, x, x.stride(0), t, m_offsets, rows, K, 2 * H, E,
+        moe_grouped_linear_wgrad(self.dgu, 2 * H, x, _row_distance(x), t, m_offsets, rows, K, 2 * H, E,
                                  self.dw_dtype, self.dw_up)
-        moe_grouped_linear_wgrad(dy, dy.stride(0), self.h, H, t, m_offsets, rows, H, K, E,
+        moe_grouped_linear_wgrad(dy, _row_distance(dy), self.h, H, t, m_offsets, rows, H, K, E,
                                  self.dw_dtype, self.dw_down)
         return self.dx, self.dw_up, self.dw_down
 

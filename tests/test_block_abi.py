@@ -304,6 +304,38 @@ def test_linear_refuses_adapters_for_another_output_before_the_product(monkeypat
             calls.clear()
 
 
+@needs_lib
+@no_gpu
+def test_runners_take_a_single_row_of_any_stride(monkeypatch):
+    """The distance of a tensor's only row to a next one says nothing (a column seen as a
+    row has 1, an expanded one 0); the rows count as whole ones."""
+    import torch
+    from quantized_moe_grouped_top_amd import runner
+    calls = {}
+    for name in ("moe_lora_add", "moe_gated_up", "moe_grouped_linear", "moe_gated_down_backward",
+                 "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad"):
+        monkeypatch.setattr(runner, name, lambda *a, name=name: calls.setdefault(name, []).append(a))
+    bf = torch.bfloat16
+    row = lambda n: torch.zeros(n, 1, dtype=bf).t()  # noqa: E731
+    x, out = row(32), row(16)
+    assert x.stride(0) == 1 and out.stride(0) == 1
+    ad = runner.LoraAdapters(1, 32, 8, 2, device="cpu")
+    a, b = torch.zeros(2, 8, 32, dtype=bf), torch.zeros(2, 16, 8, dtype=bf)
+    ad.add(x, a, b, out, torch.zeros(1, 16, dtype=bf))
+    assert calls["moe_lora_add"][0][1] == 32 and calls["moe_lora_add"][0][20] == 16
+    ffn = runner.GatedFFN(1, 32, 16, 1, train=True, device="cpu")
+    up, down = torch.zeros(1, 32, 32, dtype=bf), torch.zeros(1, 32, 16, dtype=bf)
+    ffn.forward(x, up, down)
+    ffn.backward(row(32), x, up, down)
+    assert calls["moe_gated_up"][0][1] == 32 and calls["moe_gated_down_backward"][0][1] == 32
+    of_up, of_down = calls["moe_grouped_linear_wgrad"]
+    assert of_up[3] == 32 and of_down[1] == 32
+    wide = torch.zeros(4, 64, dtype=bf)[:, :32]               # several rows: their distance
+    two = runner.GatedFFN(4, 32, 16, 1, device="cpu")
+    two.forward(wide, up, down)
+    assert calls["moe_gated_up"][1][1] == 64
+
+
 # ---- the reference ------------------------------------------------------------------
 def test_activations():
     g = np.linspace(-12, 12, 97)
