@@ -658,10 +658,10 @@ __global__ __launch_bounds__(256 * kGroups, 2) void square_kernel(const GroupedA
   const int total = __builtin_amdgcn_readfirstlane(s_seg.first[kMaxExperts]);
   const uint32_t ring = lds_addr(s_ring) + (uint32_t)(group * kSlots * kSlot);
   auto swz = [](int r) QMOE_INLINE { return (r >> 1) & 7; };
-  // 32-byte granules of an LDS row across: 16 of them for T = 256, 4 for T = 64, whose rows
+  // 32-byte granules of an LDS row across: 8 of them for T = 128, 4 for T = 64, whose rows
   // of 128 bytes take two of k into each 256 bytes of banks
   auto swt = [](int k) QMOE_INLINE {
-    return T >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+    return T == 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
   };
   typedef __attribute__((address_space(3))) s16x4 *LdsT;
   typedef __attribute__((address_space(3))) i32x4 *LdsV;
@@ -673,7 +673,7 @@ __global__ __launch_bounds__(256 * kGroups, 2) void square_kernel(const GroupedA
   };
   const uint32_t ch = (uint32_t)((g ^ swz(r16)) << 4);
   // of the lane's rows in a read across: 8 g + (r16 >> 2) and four behind it (their swizzle
-  // differs in nothing for T >= 128; for T = 64 bit 2 of k takes no part)
+  // differs in nothing for T = 128; for T = 64 bit 2 of k takes no part)
   const int kk = 8 * g + (r16 >> 2);
   const uint32_t tr = (uint32_t)(kk * kRowB + 8 * (r16 & 3)), tf = (uint32_t)swt(kk);
   const uint32_t r_rd = kRT ? tr : (uint32_t)((wm * (T / 2) + r16) * 128) + ch;

@@ -246,24 +246,24 @@ __global__ __launch_bounds__(64 * kExpandWaves, S == 4 ? 2 : 4) void expand_kern
   // the shares' sums of this thread's ranks: 4 (part + i each) ..
   auto fetch = [&](int m) QMOE_INLINE {
     const float *from = p.ws + (long long)(first + m + mine) * p.R;
+    f32x4 w[kMaxShares][kQuads];                      // all under way at once
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kTogether = 4;                      // shares whose loads are under way at once
-    for (int y0 = 0; y0 < splits; y0 += kTogether) {
-      f32x4 w[kTogether][kQuads];
+    for (int i = 0; i < kQuads; ++i) {
+      const int r = 4 * (part + i * each);
 #pragma unroll
-      for (int y = 0; y < kTogether; ++y)
+      for (int y = 0; y < kMaxShares; ++y) w[y][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (r < p.R) {
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const int r = 4 * (part + i * each);
-          w[y][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          if (y0 + y < splits && r < p.R)
-            w[y][i] = *reinterpret_cast<const f32x4 *>(from + (long long)(y0 + y) * p.max_padded * p.R + r);
-        }
+        for (int y = 0; y < kMaxShares; ++y)
+          if (y < splits)
+            w[y][i] = *reinterpret_cast<const f32x4 *>(from + (long long)y * p.max_padded * p.R + r);
+      }
+    }
 #pragma unroll
-      for (int y = 0; y < kTogether; ++y)
+    for (int i = 0; i < kQuads; ++i) {
+      v[i] = w[0][i];
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) v[i] += w[y][i];
+      for (int y = 1; y < kMaxShares; ++y) v[i] += w[y][i];
     }
   };
   fetch(0);                                           // beside the block's adapter

@@ -336,6 +336,22 @@ def test_runners_take_a_single_row_of_any_stride(monkeypatch):
     assert calls["moe_gated_up"][1][1] == 64
 
 
+@needs_lib
+def test_lora_workspace_holds_four_shares_at_most():
+    """As many as the second launch loads together."""
+    most = 0
+    for T in (1, 3, 16, 64, 200, 1000, 4096, 65536):
+        for K in (8, 512, 1024, 1536, 2048, 4096, 28672, 1 << 20):
+            for R in (8, 64, 72, 128):
+                for L in (1, 8, 128):
+                    for b in (16, 32, 64, 128, 256):
+                        one = qm.moe_align_max_padded(T, L, 1, b) * R * 4
+                        n = qm.moe_lora_workspace_bytes(T, K, R, L, b)
+                        assert n % one == 0 and 1 <= n // one <= min(4, max(1, K // 512))
+                        most = max(most, n // one)
+    assert most == 4
+
+
 # ---- the reference ------------------------------------------------------------------
 def test_activations():
     g = np.linspace(-12, 12, 97)
