@@ -287,3 +287,10 @@ def test_infinite_values_of_b(dtype, out, R):
     c.b[1, [7, 150, 64, 65, 199]] = 0.0
     finite = c.run(addend=True).double().cpu()
     assert bool(torch.isfinite(finite).all()) and torch.equal(got[:, rest], finite[:, rest])
+
+
+@pytest.mark.parametrize("T,block_m", [(255, 16), (256, 32), (1535, 32), (1536, 64)])
+def test_blocks_that_the_runner_chooses(T, block_m):
+    """Either side of each border: as with blocks given by hand, and right."""
+    assert runner.LoraAdapters(T, 136, 24, 5).block_m == block_m
+    Case(T, 136, 72, 24, 5, "bf16", "bf16", block_m, "random").check()
