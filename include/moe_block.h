@@ -46,7 +46,9 @@ extern "C" {
  * NULL stands for one expert (E = 1) with all rows.  Offsets are read on the
  * device; values outside [0, rows] count as the nearer end.  Rows that belong to
  * no expert are neither read nor written.  Sums are float32, on the matrix cores;
- * every output is rounded once, to nearest even.
+ * every output is rounded once, to nearest even.  The order of a sum hangs on the
+ * call's sizes and the expert's place: the same call repeats bit by bit, a row in
+ * another call agrees within the error of its float32 sum.
  *
  * Limits: 0 <= rows <= MOE_MAX_BLOCK_ROWS, 1 <= E <= MOE_MAX_EXPERTS; K, N and H
  * multiples of 8, at most MOE_MAX_BLOCK_WIDTH (2 H too); row distances (elements,

@@ -9,6 +9,11 @@
 // operands of a weight gradient) is copied row by row as well and its fragments are
 // read by ds_read_b64_tr_b16, which transposes 16-bit values on the way: no operand
 // is ever laid out again in memory.
+//
+// Between two products h and [dg | du] are rounded to the caller's 16-bit type: the matrix
+// instructions take no wider one, and a second part of them would double the products
+// behind and the bytes in between.  A whole pass is off by 1.41 times what the last
+// rounding alone costs (bf16 0.0024 of its rms against 0.0017, fp16 0.00029 and 0.00021).
 #include "qmoe_block.h"
 #include "qmoe_device.h"
 #include <type_traits>
@@ -910,11 +915,15 @@ hipError_t launch_stream(const GroupedArgs &a, hipStream_t s) {
 
 // Which kernel, by the experts' average rows (of one expert: its rows; of several the
 // fullest is taken to have twice the average: how the rows really lie only the device
-// knows, and what they cost, not what comes out, hangs on it).
-//   A linear of up to 64 rows: weights streamed past 16, 32 or 64 of them (up and down of
-//   one token, 4096 x 14336: 37.7 + 18.8 us, in tiles 43.3 + 57.1; 128 rows in 8 experts of
-//   4096 x 7168: 156 + 95 us with 32 rows, 192 + 107 with 16, 186 + 92 with 64, 206 + 156 in
-//   tiles; 320 rows: 205 + 103 with 64, 218 + 159 in tiles).
+// knows) and the widths.  The kernels add in orders of their own: a row of a call of other
+// rows, experts or widths, or in another expert's place, may differ in the last bits of its
+// float32 sums; the same call repeats bit by bit.  Other splits of the rows cost time only:
+// 2048 -> 1024, 4096 rows in 128 experts 131 us, half of them in one 205, all 308 (alone, as
+// one expert, 25); 4096 -> 7168, 128 rows in 8 experts 88, half in one 93, all 40.
+//   A linear of up to 64 rows of one expert, or 48 on average of several: weights streamed
+//   past 16, 32 or 64 of them (up and down of one token, 4096 x 14336: 37.7 + 18.8 us, in tiles
+//   43.3 + 57.1; 128 rows in 8 experts of 4096 x 7168: 156 + 95 us with 32 rows, 192 + 107 with
+//   16, 186 + 92 with 64, 206 + 156 in tiles; 320 rows: 205 + 103 with 64, 218 + 159 in tiles).
 //   Else 256 x 256 tiles where half of the CUs have one (E = 8, rows of 2048 x 4096 x 14336:
 //   128 tiles of the linear back down 366 us, with 128 x 128 499; 777 x 1024 x 3584, 70 tiles,
 //   28 us, with 128 x 128 16), 128 x 128 where these are 192 at least, 64 x 64 below (777 x

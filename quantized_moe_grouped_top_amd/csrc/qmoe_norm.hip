@@ -4,8 +4,10 @@
 // Memory streams: a workgroup holds a whole row in registers (eight columns a
 // thread and chunk, 16-byte loads and stores), so every byte is read and written
 // once; the two sums of a row go through one wavefront reduction and LDS.  4096 rows of
-// 4096 with two slots, norms before and after (168 MB): 29.5 us, 5.7 TB/s; the gradients
-// of 8192 rows of 6144 (604 MB): 138 us with the weights' sums, 5 of them, 4.4 TB/s.
+// 4096 with two slots, norms before and after (168 MB): 32.5 us a call among others, the
+// kernel 30.5 (29.4 at least), 5.5 TB/s; the gradients of 8192 rows of 6144 (604 MB): 138
+// us a call, 4.4 TB/s, 5 of them the weights' sums (traced launch by launch, which starts
+// each with the card empty, 147 + 5, at least 138 + 4.7).
 #include "qmoe_block.h"
 #include "qmoe_device.h"
 
