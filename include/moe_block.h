@@ -114,7 +114,8 @@ size_t moe_lora_workspace_bytes(int T, int K, int R, int L, int block_m);
  * its value is left out at most; three parts where out is float32, 2^-24).  In
  * fp16 up to 2^-39 of the token's largest inner value is left out of each besides,
  * which is less down to values of 2^-23 (float32: 2^-15) of the largest.
- * Infinities of x, a and b count as in the definition.  The result is rounded once.
+ * Infinities of x, a and b count as in the definition (an inner value that is left
+ * out whole as a 0).  The result is rounded once.
  *
  *   x       [T, K] of type dtype (MOE_BF16, MOE_F16), rows ldx elements apart
  *   a       [L, R, K], b [L, N, R] of type dtype

@@ -20,14 +20,18 @@ def _sigmoid(z):
 
 
 def act(g, kind):
-    """act(g) and its derivative."""
+    """act(g) and its derivative; their limits at infinite g."""
     g = np.asarray(g, np.float64)
     if kind == SILU:
-        s = _sigmoid(g)
-        return g * s, s * (1.0 + g * (1.0 - s))
-    # (1 + tanh(v)) / 2 = sigmoid(2 v), which does not cancel where tanh is nearly -1
-    s = _sigmoid(2.0 * _C * (g + 0.044715 * g ** 3))
-    return g * s, s + g * s * (1.0 - s) * 2.0 * _C * (1.0 + 3.0 * 0.044715 * g * g)
+        z, dz = g, 1.0
+    else:
+        # (1 + tanh(v)) / 2 = sigmoid(2 v), which does not cancel where tanh is nearly -1
+        z = 2.0 * _C * (g + 0.044715 * g ** 3)
+        dz = 2.0 * _C * (1.0 + 3.0 * 0.044715 * g * g)
+    s = _sigmoid(z)
+    with np.errstate(invalid="ignore"):
+        a, da = g * s, s + g * s * (1.0 - s) * dz
+    return np.where(g == -np.inf, 0.0, a), np.where(np.isinf(g), g > 0, da)
 
 
 def segments(offsets, rows):

@@ -363,6 +363,15 @@ def test_activations():
         assert abs(a[48]) == 0 and a[-1] == pytest.approx(12.0, rel=1e-4) and abs(a[0]) < 1e-4
 
 
+@pytest.mark.parametrize("kind", [B.SILU, B.GELU])
+def test_activations_at_the_ends(kind):
+    far, inf = np.array([-1e4, 1e4]), np.array([-np.inf, np.inf])
+    for x in (far, inf):
+        a, da = B.act(x, kind)
+        assert a.tolist() == [0.0, x[1]] and da.tolist() == [0.0, 1.0]
+    assert np.isnan(B.act(np.array([np.nan]), kind)).all()
+
+
 def _numeric(f, v, d=1e-6):
     """Central differences of the scalar f with respect to every element of v."""
     out = np.zeros_like(v)
